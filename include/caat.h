@@ -444,6 +444,224 @@ CAAT_API caat_status caat_permute_weights(const caat_bf16* W, caat_bf16* W_out, 
 CAAT_API caat_status caat_speedup_model(double h, double s, double r, double p, double C, double* speedup_out,
                                         double* p_star_out);
 
+/*
+ * The attention block in front of the row-parallel output projection (§3.1 Eq. 6 and App. A
+ * Eq. 18-19, 23-24: rank m computes the heads it owns from its own input; their outputs, side by
+ * side, are the X_m [T, K/P] of caat_rowpar_forward with K / P = heads_q * dh).  The paper fixes
+ * neither the positions nor the attention kernel; the four operators below are the usual ones of a
+ * decoder, for P ranks side by side like every call of this library:
+ *
+ *   caat_rope          rotary positions of q and k, or of q with k and v appended to a cache
+ *   caat_attn_forward  causal attention over packed prompts, heads_q / heads_k queries per key head
+ *   caat_attn_backward its gradients
+ *   caat_attn_decode   one token per sequence against a cache
+ *
+ * Strides: *_stride_rank and *_stride_token count elements between ranks and tokens, so that q, k
+ * and v may be views of one fused projection [P, T, (heads_q + 2 heads_k) dh]; within a token the
+ * heads are dh apart and a head is contiguous.  Both 0: a contiguous [P, T, heads, dh].  Strides are
+ * multiples of 8 elements.
+ */
+
+/* Frequency scalings of caat_rope_frequencies for contexts longer than the trained one. */
+#define CAAT_ROPE_SCALING_NONE 0
+#define CAAT_ROPE_SCALING_LINEAR 1 /* position interpolation: f_j / factor */
+#define CAAT_ROPE_SCALING_NTK 2    /* theta raised by factor^(rot / (rot - 2)): the slowest pair is
+                                      slowed by `factor`, the fastest keeps its speed */
+#define CAAT_ROPE_SCALING_YARN 3   /* per pair between f_j / factor (fewer than 1 turn over the
+                                      trained length) and f_j (more than 32 turns), linear in the
+                                      number of turns; vectors scaled by 0.1 ln(factor) + 1 */
+
+/*
+ * caat_rope_frequencies - host only: the rotation per position (radians) of the rot / 2 pairs,
+ * f_j = theta^(-2 j / rot), scaled as above, and the factor on the rotated vectors.
+ *   rot      rotated elements of a head, even, 2..256 (4.. for NTK)
+ *   theta    > 1;  factor >= 1 and trained_length > 0 (YARN) are ignored where they play no part
+ *   inv_freq host, rot / 2 doubles (out);  mscale_out may be NULL
+ */
+CAAT_API caat_status caat_rope_frequencies(int rot, double theta, int scaling, double factor, double trained_length,
+                                           double* inv_freq, float* mscale_out);
+
+#define CAAT_ROPE_FLAG_INTERLEAVED 0x1u /* pairs (2 j, 2 j + 1); default: (j, j + rot / 2) */
+#define CAAT_ROPE_FLAG_BACKWARD 0x2u    /* rotate by the negative angle: the gradient of the call
+                                           (mscale multiplies there too) */
+
+/*
+ * caat_rope - rotary positions.  With t = position * inv_freq[j] (evaluated in double, so far
+ * positions keep their angle), pair (a, b) of every head becomes
+ *   (mscale (a cos t - b sin t), mscale (b cos t + a sin t)),
+ * in fp32, rounded once; elements rot..dh-1 of a head are copied.
+ *
+ *   q, k       device bf16 [P, T, heads_q | heads_k, dh], strided as above; heads_q or heads_k may
+ *              be 0 (the pointer is then ignored)
+ *   q_out      device bf16 [P, T, heads_q, dh] contiguous, or q itself (in place, q's strides)
+ *   slots      NULL: k_out is [P, T, heads_k, dh] contiguous or k itself.
+ *              Else device int64 [T]: token t's rotated k goes to row slots[t] of k_out
+ *              [P, cache_rows, heads_k, dh] and its v, unchanged, to the same row of v_out; slot -1
+ *              skips the token's k and v (padding).  Any other slot outside [0, cache_rows) is
+ *              skipped too and reported by caat_get_device_status as CAAT_ERR_INVALID_ARG.  Two
+ *              tokens must not share a slot (which of them a row then holds is unspecified).
+ *              Rows without a token keep their contents.
+ *   v, v_out   only with slots
+ *   positions  device int32 [T], shared by the ranks; NULL: 0..T-1
+ *   inv_freq   HOST, rot / 2 doubles, finite; read before return
+ *   rot        0 < rot <= dh; rot % 16 == 0 (interleaved: rot % 8 == 0)
+ *   dh         dh % 8 == 0, dh <= 256
+ * Outputs that are not in place must not overlap the inputs.  Pointers 16-byte aligned.
+ */
+typedef struct caat_rope_args {
+  const caat_bf16* q;
+  const caat_bf16* k;
+  const caat_bf16* v;
+  caat_bf16* q_out;
+  caat_bf16* k_out;
+  caat_bf16* v_out;
+  const int32_t* positions;
+  const int64_t* slots;
+  const double* inv_freq;      /* host */
+  caat_stream_t stream;
+  caat_timing* timing;
+  int64_t T, cache_rows;
+  int64_t q_stride_rank, q_stride_token;
+  int64_t k_stride_rank, k_stride_token;
+  int64_t v_stride_rank, v_stride_token;
+  int32_t P, heads_q, heads_k, dh, rot;
+  float mscale;
+  uint32_t flags;              /* CAAT_ROPE_FLAG_* */
+} caat_rope_args;
+
+CAAT_API caat_status caat_rope(const caat_rope_args* args);
+
+/*
+ * caat_attn_forward - causal attention over packed sequences, on every rank.  Sequence s owns the
+ * queries [cu_q[s], cu_q[s+1]) and the keys [cu_k[s], cu_k[s+1]); its last query sees its last key,
+ * so query i of n sees the first i + 1 + (m - n) of m keys (m > n: a cached prefix; m < n: the first
+ * queries see none).  Query head h reads key head h / (heads_q / heads_k).
+ *   S = scale q k^T over the visible keys, out = softmax(S) v, lse = log(sum exp S)
+ * with S, the softmax and the sums in fp32; the probabilities are rounded to bf16 for the product
+ * with v.  A row that sees no key gives out = 0 and lse = -inf.  Rows of out and lse behind the last
+ * sequence are not written.  Values of k and v outside a sequence's keys never reach its rows.
+ *
+ *   q          device bf16 [P, Tq, heads_q, dh], strided
+ *   k, v       device bf16 [P, Tk, heads_k, dh], strided
+ *   out        device bf16 [P, Tq, heads_q * dh] contiguous; must not overlap the inputs
+ *   lse        device fp32 [P, heads_q, Tq], or NULL
+ *   cu_q, cu_k HOST int32 [n_seq + 1], non-decreasing, from >= 0 up to <= Tq | Tk; cu_k NULL: cu_q.
+ *              Read before return.
+ *   dh         dh % 8 == 0, dh <= 128;  heads_q % heads_k == 0;  scale > 0, finite
+ *   workspace  caat_attn_workspace_size(..., CAAT_VARIANT_ATTN) bytes, 256-byte aligned; NULL when
+ *              that is 0.  Clobbered.
+ * Capturable in a CUDA graph (which then holds the offsets of the captured call).
+ */
+typedef struct caat_attn_args {
+  const caat_bf16* q;
+  const caat_bf16* k;
+  const caat_bf16* v;
+  caat_bf16* out;
+  float* lse;
+  const int32_t* cu_q;         /* host */
+  const int32_t* cu_k;         /* host, or NULL */
+  void* workspace;
+  size_t ws_bytes;
+  caat_stream_t stream;
+  caat_timing* timing;
+  int64_t Tq, Tk;
+  int64_t q_stride_rank, q_stride_token;
+  int64_t k_stride_rank, k_stride_token;
+  int64_t v_stride_rank, v_stride_token;
+  int32_t n_seq, P, heads_q, heads_k, dh;
+  float scale;
+  uint32_t flags;              /* 0 */
+} caat_attn_args;
+
+CAAT_API caat_status caat_attn_forward(const caat_attn_args* args);
+
+/*
+ * caat_attn_backward - gradients of caat_attn_forward.  With P the probabilities (recomputed from lse),
+ * D = rowsum(dout * out):
+ *   dv = P^T dout,  dS = scale P (dout v^T - D),  dq = dS k,  dk = dS^T q,
+ * sums in fp32 (over the queries of every head that shares a key head, too, in a fixed order: results
+ * do not change from run to run); P and dS are rounded to bf16 as operands of the products.
+ *
+ *   q, k, v, cu_q, cu_k, scale, sizes  as in the forward
+ *   out, lse    the forward's results;  dout  device bf16 [P, Tq, heads_q * dh]
+ *   dq [P, Tq, heads_q, dh], dk, dv [P, Tk, heads_k, dh]  device bf16, contiguous (out).  Keys that no
+ *               query sees get zeros; rows outside every sequence are not written.
+ *   workspace   caat_attn_workspace_size(..., CAAT_VARIANT_ATTN_BWD) bytes, 256-byte aligned
+ * Outputs must not overlap the inputs or each other.
+ */
+typedef struct caat_attn_bwd_args {
+  const caat_bf16* q;
+  const caat_bf16* k;
+  const caat_bf16* v;
+  const caat_bf16* out;
+  const float* lse;
+  const caat_bf16* dout;
+  caat_bf16* dq;
+  caat_bf16* dk;
+  caat_bf16* dv;
+  const int32_t* cu_q;         /* host */
+  const int32_t* cu_k;         /* host, or NULL */
+  void* workspace;
+  size_t ws_bytes;
+  caat_stream_t stream;
+  caat_timing* timing;
+  int64_t Tq, Tk;
+  int64_t q_stride_rank, q_stride_token;
+  int64_t k_stride_rank, k_stride_token;
+  int64_t v_stride_rank, v_stride_token;
+  int32_t n_seq, P, heads_q, heads_k, dh;
+  float scale;
+  uint32_t flags;              /* 0 */
+} caat_attn_bwd_args;
+
+CAAT_API caat_status caat_attn_backward(const caat_attn_bwd_args* args);
+
+/*
+ * caat_attn_decode - attention of one new token per sequence over its cache, on every rank:
+ * out[b] = softmax(scale q[b] K[b, :n]^T) V[b, :n], n = lens[b] (the new token's own key included, as
+ * caat_rope appended it).  out is the X of caat_rowpar_forward for T = B tokens.
+ *   q                device bf16 [P, B, heads_q, dh], strided (q_stride_token between sequences)
+ *   k_cache, v_cache device bf16 [P, B, capacity, heads_k, dh] contiguous
+ *   lens             DEVICE int32 [B] (it grows from step to step of a captured graph).  0 gives
+ *                    out = 0; a length outside [0, capacity] does too, and is reported by
+ *                    caat_get_device_status as CAAT_ERR_INVALID_ARG.  Cache rows from lens[b] on are
+ *                    never used, whatever they hold.
+ *   out              device bf16 [P, B, heads_q * dh] contiguous; must not overlap the inputs
+ *   workspace        caat_attn_workspace_size(B, capacity, ..., CAAT_VARIANT_ATTN_DECODE) bytes, 256-byte
+ *                    aligned; two calls that may overlap on the GPU need one each
+ *   dh, heads, scale as in caat_attn_forward
+ * Deterministic; capturable.
+ */
+typedef struct caat_attn_decode_args {
+  const caat_bf16* q;
+  const caat_bf16* k_cache;
+  const caat_bf16* v_cache;
+  const int32_t* lens;
+  caat_bf16* out;
+  void* workspace;
+  size_t ws_bytes;
+  caat_stream_t stream;
+  caat_timing* timing;
+  int64_t B, capacity;
+  int64_t q_stride_rank, q_stride_token;
+  int32_t P, heads_q, heads_k, dh;
+  float scale;
+  uint32_t flags;              /* 0 */
+} caat_attn_decode_args;
+
+CAAT_API caat_status caat_attn_decode(const caat_attn_decode_args* args);
+
+/* Workspace variants of caat_attn_workspace_size. */
+#define CAAT_VARIANT_ATTN 0
+#define CAAT_VARIANT_ATTN_BWD 1
+#define CAAT_VARIANT_ATTN_DECODE 2
+
+/* Bytes of device workspace an attention call of this shape needs (SIZE_MAX for invalid sizes).
+ * CAAT_VARIANT_ATTN and _BWD: Tq, Tk, n_seq as in the call; CAAT_VARIANT_ATTN_DECODE: Tq = B,
+ * Tk = capacity, n_seq is not used. */
+CAAT_API size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int heads_q, int heads_k, int dh,
+                                         int variant);
+
 /* Bytes of device workspace a forward call of this shape needs (0 for invalid shapes is
  * never returned: invalid shapes give SIZE_MAX).  variant: CAAT_VARIANT_*; for the MLP
  * variant K is F. */

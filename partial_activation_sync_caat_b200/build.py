@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcaat.so")
 
-SOURCES = ["caat_api.cu"]
+SOURCES = ["caat_api.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -48,16 +49,25 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and up_to_date():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
-           "-DCAAT_BUILD", "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
+    base = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
+            "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC, "-DCAAT_BUILD"]
     if verbose_ptxas:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if verbose_ptxas:
-        sys.stderr.write(res.stdout + res.stderr)
+        base.insert(1, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory() as objs:  # the sources compile side by side, then link
+        jobs = []
+        for src in SOURCES:
+            cmd = base + ["-c", os.path.join(CSRC, src), "-o", os.path.join(objs, src + ".o")]
+            jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        outs = [(cmd, p.communicate()[0], p.returncode) for cmd, p in jobs]
+        if all(rc == 0 for _, _, rc in outs):
+            cmd = base + ["-shared", "-o", tmp] + [os.path.join(objs, src + ".o") for src in SOURCES]
+            res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+            outs.append((cmd, res.stdout, res.returncode))
+    for cmd, text, rc in outs:
+        if rc != 0:
+            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + text)
+        if verbose_ptxas:
+            sys.stderr.write(text)
     os.replace(tmp, LIB)
     return LIB
 

@@ -42,6 +42,16 @@ CAAT_FLAG_NORM_BESIDE_GEMM = 0x200
 
 CAAT_NOALLOC_SCRATCH_BYTES = 1048576
 
+CAAT_ROPE_SCALING_NONE = 0
+CAAT_ROPE_SCALING_LINEAR = 1
+CAAT_ROPE_SCALING_NTK = 2
+CAAT_ROPE_SCALING_YARN = 3
+CAAT_ROPE_FLAG_INTERLEAVED = 0x1
+CAAT_ROPE_FLAG_BACKWARD = 0x2
+CAAT_VARIANT_ATTN = 0
+CAAT_VARIANT_ATTN_BWD = 1
+CAAT_VARIANT_ATTN_DECODE = 2
+
 # Every symbol include/caat.h declares (checked by the ABI tests).
 EXPORTS = [
     "caat_rowpar_forward", "caat_rowpar_forward_ex", "caat_rowpar_forward_host",
@@ -51,6 +61,8 @@ EXPORTS = [
     "caat_version", "caat_permute_weights", "caat_speedup_model", "caat_rowpar_backward",
     "caat_plan_create", "caat_plan_execute", "caat_plan_destroy", "caat_rowpar_tp_local",
     "caat_rowpar_tp_finish", "caat_rowpar_tp_local_push", "caat_rowpar_tp_reduce", "caat_rowpar_tp_finish_wait",
+    "caat_rope_frequencies", "caat_rope", "caat_attn_forward", "caat_attn_backward", "caat_attn_decode",
+    "caat_attn_workspace_size",
 ]
 
 CAAT_TP_MAX_WORLD = 8
@@ -117,6 +129,52 @@ class MlpArgs(ctypes.Structure):
     ]
 
 
+class RopeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p), ("stream", ctypes.c_void_p),
+        ("timing", ctypes.c_void_p), ("T", ctypes.c_int64), ("cache_rows", ctypes.c_int64),
+        ("q_stride_rank", ctypes.c_int64), ("q_stride_token", ctypes.c_int64), ("k_stride_rank", ctypes.c_int64),
+        ("k_stride_token", ctypes.c_int64), ("v_stride_rank", ctypes.c_int64), ("v_stride_token", ctypes.c_int64),
+        ("P", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("dh", ctypes.c_int32),
+        ("rot", ctypes.c_int32), ("mscale", ctypes.c_float), ("flags", ctypes.c_uint32),
+    ]
+
+
+_ATTN_TAIL = [
+    ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+    ("ws_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p), ("timing", ctypes.c_void_p),
+    ("Tq", ctypes.c_int64), ("Tk", ctypes.c_int64), ("q_stride_rank", ctypes.c_int64),
+    ("q_stride_token", ctypes.c_int64), ("k_stride_rank", ctypes.c_int64), ("k_stride_token", ctypes.c_int64),
+    ("v_stride_rank", ctypes.c_int64), ("v_stride_token", ctypes.c_int64), ("n_seq", ctypes.c_int32),
+    ("P", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("dh", ctypes.c_int32),
+    ("scale", ctypes.c_float), ("flags", ctypes.c_uint32),
+]
+
+
+class AttnArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)] + _ATTN_TAIL
+
+
+class AttnBwdArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dout", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+                ("dv", ctypes.c_void_p)] + _ATTN_TAIL
+
+
+class AttnDecodeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p), ("timing", ctypes.c_void_p), ("B", ctypes.c_int64), ("capacity", ctypes.c_int64),
+        ("q_stride_rank", ctypes.c_int64), ("q_stride_token", ctypes.c_int64), ("P", ctypes.c_int32),
+        ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32), ("dh", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("flags", ctypes.c_uint32),
+    ]
+
+
 _lib = None
 
 
@@ -162,6 +220,14 @@ def lib() -> ctypes.CDLL:
     L.caat_rowpar_backward.argtypes = [ctypes.POINTER(BwdArgs)]
     L.caat_speedup_model.restype = ctypes.c_int
     L.caat_speedup_model.argtypes = [dbl, dbl, dbl, dbl, dbl, ctypes.POINTER(dbl), ctypes.POINTER(dbl)]
+    L.caat_rope_frequencies.argtypes = [ctypes.c_int, dbl, ctypes.c_int, dbl, dbl, vp, ctypes.POINTER(ctypes.c_float)]
+    L.caat_rope_frequencies.restype = ctypes.c_int
+    for name, args in (("caat_rope", RopeArgs), ("caat_attn_forward", AttnArgs), ("caat_attn_backward", AttnBwdArgs),
+                       ("caat_attn_decode", AttnDecodeArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(args)]
+        getattr(L, name).restype = ctypes.c_int
+    L.caat_attn_workspace_size.argtypes = [i64, i64] + [ctypes.c_int] * 6
+    L.caat_attn_workspace_size.restype = sz
     L.caat_permute_weights.restype = ctypes.c_int
     L.caat_permute_weights.argtypes = [vp, vp, vp, dbl, ctypes.c_int, i64, i64, vp]
     L.caat_sync_mask.restype = ctypes.c_int
@@ -518,6 +584,275 @@ def caat_rowpar_backward(X, W, h, gamma, dout, sync_idx, P: int, p: float, dX, d
     a.P = P
     a.flags = int(flags)
     _check(lib().caat_rowpar_backward(ctypes.byref(a)), "caat_rowpar_backward")
+
+
+# ---------------------------------------------------------------------------------------
+# the attention block: rotary positions, causal attention, decoding
+# ---------------------------------------------------------------------------------------
+
+_ROPE_SCALINGS = {"none": CAAT_ROPE_SCALING_NONE, "linear": CAAT_ROPE_SCALING_LINEAR, "ntk": CAAT_ROPE_SCALING_NTK,
+                  "yarn": CAAT_ROPE_SCALING_YARN}
+
+
+def caat_rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                          trained_length: float = 4096.0):
+    """(frequencies float64[rot / 2], mscale): the rotation per position of each pair, scaled for
+    contexts longer than the trained one ("none", "linear", "ntk", "yarn"), and the factor on the
+    rotated vectors.  Host only."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    f = np.zeros(max(int(rot), 2) // 2, dtype=np.float64)
+    m = ctypes.c_float(1.0)
+    _check(lib().caat_rope_frequencies(int(rot), float(theta), _ROPE_SCALINGS[scaling], float(factor),
+                                       float(trained_length), f.ctypes.data, ctypes.byref(m)), "caat_rope_frequencies")
+    return f, float(m.value)
+
+
+def _on_current_device(dev):
+    """The library queues on the current device: tensors of another one are refused."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _like(t, name, dtype, shape, device, contiguous=True):
+    """Address of a tensor after checks of its type, shape, device and layout."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _heads4(t, name, dtype, device, shape=None):
+    """Address and (rank, token) strides of a [P, T, heads, dh] tensor whose heads lie side by side
+    within a token (a contiguous tensor, or a slice of a fused projection)."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [P, T, heads, dh]")
+    ptr = _like(t, name, dtype, tuple(t.shape) if shape is None else shape, device, contiguous=False)
+    if t.is_contiguous():
+        return ptr, t.shape[1] * t.shape[2] * t.shape[3], t.shape[2] * t.shape[3]
+    s = t.stride()
+    if (t.shape[3] > 1 and s[3] != 1) or (t.shape[2] > 1 and s[2] != t.shape[3]):
+        raise ValueError(f"{name}: the heads of a token must be contiguous and side by side")
+    # a dimension of one element has no stride of its own
+    token = s[1] if t.shape[1] > 1 else t.shape[2] * t.shape[3]
+    return ptr, s[0] if t.shape[0] > 1 else max(s[0], token * t.shape[1]), token
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """(tensor or None, address, bytes) of a call's workspace; one allocated here is kept from
+    reuse until a stream other than the current one has finished with it."""
+    import torch
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = alloc_workspace(nbytes, device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not {device}")
+    return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _offsets(cu, name):
+    """Host int32 offsets from a sequence, an array or a CPU tensor."""
+    arr = np.asarray(cu)
+    if arr.ndim != 1 or arr.size < 1 or arr.dtype.kind not in "iu":
+        raise ValueError(f"{name} must be a one-dimensional host array of integers")
+    if arr.dtype != np.int32:
+        if arr.size and (arr.min() < 0 or arr.max() > 2**31 - 1):
+            raise CaatError(CAAT_ERR_INVALID_ARG, name)
+        arr = arr.astype(np.int32)
+    return np.ascontiguousarray(arr)
+
+
+def caat_attn_workspace_size(Tq: int, Tk: int, n_seq: int, P: int, heads_q: int, heads_k: int, dh: int,
+                             variant: int = CAAT_VARIANT_ATTN) -> int:
+    n = lib().caat_attn_workspace_size(int(Tq), int(Tk), int(n_seq), int(P), int(heads_q), int(heads_k), int(dh),
+                                       int(variant))
+    if n == ctypes.c_size_t(-1).value:
+        raise CaatError(CAAT_ERR_INVALID_ARG, "caat_attn_workspace_size")
+    return int(n)
+
+
+def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved, backward, mscale, stream, timing):
+    import torch
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("caat_rope: q and k are both None")
+    dev = first.device
+    _on_current_device(dev)
+    bf = torch.bfloat16
+    a = RopeArgs()
+    a.P, a.T, a.dh = int(first.shape[0]), int(first.shape[1]), int(first.shape[3])
+
+    def out_ptr(o, x, name):
+        if o is x or (o.data_ptr() == x.data_ptr() and o.stride() == x.stride() and o.shape == x.shape):
+            return _like(o, name, bf, tuple(x.shape), dev, contiguous=False)
+        if o.data_ptr() == x.data_ptr() and o.numel():
+            raise ValueError(f"{name} in place must have its input's shape and strides")
+        return _like(o, name, bf, tuple(x.shape), dev)
+
+    if q is not None:
+        a.heads_q = int(q.shape[2])
+        a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
+        a.q_out = out_ptr(q_out, q, "q_out")
+    if k is not None:
+        a.heads_k = int(k.shape[2])
+        a.k, a.k_stride_rank, a.k_stride_token = _heads4(k, "k", bf, dev, (a.P, a.T, a.heads_k, a.dh))
+        if slots is None:
+            a.k_out = out_ptr(k_out, k, "k_out")
+        else:
+            a.v, a.v_stride_rank, a.v_stride_token = _heads4(v, "v", bf, dev, (a.P, a.T, a.heads_k, a.dh))
+            a.cache_rows = int(k_out.numel() // (a.P * a.heads_k * a.dh))
+            cache = (a.P, a.cache_rows, a.heads_k, a.dh)
+            slab = tuple(k_out.shape)
+            if k_out.dim() == 5 and slab[:1] + slab[3:] == (a.P, a.heads_k, a.dh):
+                cache = slab
+            a.k_out = _like(k_out, "k_cache", bf, cache, dev)
+            a.v_out = _like(v_out, "v_cache", bf, cache, dev)
+            a.slots = _like(slots, "slots", torch.int64, (a.T,), dev)
+    if positions is not None:
+        a.positions = _like(positions, "positions", torch.int32, (a.T,), dev)
+    freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+    if freq.ndim != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    a.inv_freq, a.rot = freq.ctypes.data, 2 * freq.size
+    a.stream = _stream_ptr(stream)
+    a.timing = timing.handle if timing is not None else None
+    a.mscale = float(mscale)
+    a.flags = (CAAT_ROPE_FLAG_INTERLEAVED if interleaved else 0) | (CAAT_ROPE_FLAG_BACKWARD if backward else 0)
+    _check(lib().caat_rope(ctypes.byref(a)), "caat_rope")
+
+
+def caat_rope(q, k, positions, inv_freq, *, q_out, k_out, interleaved: bool = False, backward: bool = False,
+              mscale: float = 1.0, stream=None, timing=None):
+    """Queues the rotation of q [P,T,heads_q,dh] and k [P,T,heads_k,dh] (bf16; either may be None, and
+    may be a slice of a fused projection) by their positions (CUDA int32 [T], or None: 0..T-1).
+
+    inv_freq: host float64 [rot / 2] (caat_rope_frequencies); the first rot elements of a head turn.
+    q_out, k_out: contiguous, or q and k themselves (in place).  backward: by the negative angle, the
+    gradient of the same call."""
+    _rope(q, k, None, positions, None, inv_freq, q_out, k_out, None, interleaved, backward, mscale, stream, timing)
+    return q_out, k_out
+
+
+def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q_out=None, interleaved: bool = False,
+                     backward: bool = False, mscale: float = 1.0, stream=None, timing=None):
+    """As caat_rope, with the rotated k and v of token t written to row slots[t] (CUDA int64 [T]; -1:
+    not written) of the caches [P,rows,heads_k,dh] (or [P,B,capacity,heads_k,dh], row = b * capacity +
+    position).  Slots outside the cache are skipped and reported by caat_get_device_status."""
+    if k is None or v is None or slots is None:
+        raise ValueError("caat_rope_append needs k, v and slots")
+    _rope(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, interleaved, backward, mscale, stream, timing)
+    return q_out
+
+
+def _attn_common(a, q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
+    """Fills the arguments the forward and the backward share; returns what must outlive the call."""
+    import torch
+    dev = q.device
+    _on_current_device(dev)
+    bf = torch.bfloat16
+    a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
+    a.P, a.Tq, a.heads_q, a.dh = (int(x) for x in q.shape)
+    a.k, a.k_stride_rank, a.k_stride_token = _heads4(k, "k", bf, dev)
+    a.Tk, a.heads_k = int(k.shape[1]), int(k.shape[2])
+    if k.shape[0] != a.P or k.shape[3] != a.dh:
+        raise ValueError("q and k must have the same ranks and head size")
+    a.v, a.v_stride_rank, a.v_stride_token = _heads4(v, "v", bf, dev, tuple(k.shape))
+    cq = _offsets(cu_q, "cu_q")
+    ck = None if cu_k is None else _offsets(cu_k, "cu_k")
+    if ck is not None and ck.size != cq.size:
+        raise ValueError("cu_q and cu_k must have the same length")
+    a.cu_q, a.n_seq = cq.ctypes.data, cq.size - 1
+    a.cu_k = None if ck is None else ck.ctypes.data
+    a.scale = float(scale) if scale is not None else a.dh ** -0.5
+    a.stream = _stream_ptr(stream)
+    a.timing = timing.handle if timing is not None else None
+    need = lib().caat_attn_workspace_size(a.Tq, a.Tk, a.n_seq, a.P, a.heads_q, a.heads_k, a.dh, variant)
+    if need == ctypes.c_size_t(-1).value:
+        need = 0  # sizes the call itself refuses
+    ws, a.workspace, a.ws_bytes = _workspace(workspace, need, dev, stream)
+    return cq, ck, ws
+
+
+def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optional[float] = None, workspace=None,
+                      stream=None, timing=None):
+    """Queues causal attention over packed sequences on every rank.
+
+    q [P,Tq,heads_q,dh], k, v [P,Tk,heads_k,dh] (bf16, contiguous or slices of a fused projection);
+    cu_q, cu_k: host offsets [n_seq + 1] of the sequences' queries and keys (cu_k None: cu_q; the last
+    query sees the last key); out [P,Tq,heads_q*dh] bf16, the X of caat_rowpar_forward; lse
+    [P,heads_q,Tq] fp32, needed by the backward.  scale None: dh ** -0.5."""
+    import torch
+    a = AttnArgs()
+    keep = _attn_common(a, q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN, workspace, stream, timing)
+    a.out = _like(out, "out", torch.bfloat16, (a.P, a.Tq, a.heads_q * a.dh), q.device)
+    if lse is not None:
+        a.lse = _like(lse, "lse", torch.float32, (a.P, a.heads_q, a.Tq), q.device)
+    _check(lib().caat_attn_forward(ctypes.byref(a)), "caat_attn_forward")
+    del keep
+    return out
+
+
+def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, scale: Optional[float] = None,
+                       workspace=None, stream=None, timing=None):
+    """Queues the gradients of caat_attn_forward: dq [P,Tq,heads_q,dh], dk, dv [P,Tk,heads_k,dh] (bf16,
+    contiguous) from the forward's inputs, its out and lse, and dout [P,Tq,heads_q*dh]."""
+    import torch
+    a = AttnBwdArgs()
+    keep = _attn_common(a, q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN_BWD, workspace, stream, timing)
+    dev, bf = q.device, torch.bfloat16
+    a.out = _like(out, "out", bf, (a.P, a.Tq, a.heads_q * a.dh), dev)
+    a.dout = _like(dout, "dout", bf, (a.P, a.Tq, a.heads_q * a.dh), dev)
+    a.lse = _like(lse, "lse", torch.float32, (a.P, a.heads_q, a.Tq), dev)
+    a.dq = _like(dq, "dq", bf, tuple(q.shape), dev)
+    a.dk = _like(dk, "dk", bf, tuple(k.shape), dev)
+    a.dv = _like(dv, "dv", bf, tuple(k.shape), dev)
+    _check(lib().caat_attn_backward(ctypes.byref(a)), "caat_attn_backward")
+    del keep
+    return dq, dk, dv
+
+
+def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] = None, workspace=None, stream=None,
+                     timing=None):
+    """Queues attention of one new token per sequence over its cache on every rank.
+
+    q [P,B,heads_q,dh], caches [P,B,capacity,heads_k,dh] (bf16), lens CUDA int32 [B] (keys of each
+    sequence, the new token's included), out [P,B,heads_q*dh]: the X of caat_rowpar_forward."""
+    import torch
+    dev, bf = q.device, torch.bfloat16
+    _on_current_device(dev)
+    a = AttnDecodeArgs()
+    a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
+    a.P, a.B, a.heads_q, a.dh = (int(x) for x in q.shape)
+    if k_cache.dim() != 5:
+        raise ValueError("k_cache must be [P, B, capacity, heads_k, dh]")
+    a.capacity, a.heads_k = int(k_cache.shape[2]), int(k_cache.shape[3])
+    cache = (a.P, a.B, a.capacity, a.heads_k, a.dh)
+    a.k_cache = _like(k_cache, "k_cache", bf, cache, dev)
+    a.v_cache = _like(v_cache, "v_cache", bf, cache, dev)
+    a.lens = _like(lens, "lens", torch.int32, (a.B,), dev)
+    a.out = _like(out, "out", bf, (a.P, a.B, a.heads_q * a.dh), dev)
+    a.scale = float(scale) if scale is not None else a.dh ** -0.5
+    a.stream = _stream_ptr(stream)
+    a.timing = timing.handle if timing is not None else None
+    need = lib().caat_attn_workspace_size(a.B, a.capacity, 0, a.P, a.heads_q, a.heads_k, a.dh,
+                                          CAAT_VARIANT_ATTN_DECODE)
+    if need == ctypes.c_size_t(-1).value:
+        need = 0
+    keep, a.workspace, a.ws_bytes = _workspace(workspace, need, dev, stream)
+    _check(lib().caat_attn_decode(ctypes.byref(a)), "caat_attn_decode")
+    del keep
+    return out
 
 
 def caat_rowpar_forward_host(X, W, residual, gamma, sync_idx, P: int, p: float, out, workspace, *,

@@ -1,0 +1,362 @@
+// attn_api.cu - host side of the attention block's calls in include/caat.h (rotary positions, packed
+// causal attention and its gradients, decoding): argument validation, work lists and launches.
+// The device code lives in the *.cuh files included below.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "caat.h"
+#include "host_common.h"
+#include "ptx.cuh"
+#include "attn_simple.cuh"
+#include "rope.cuh"
+
+namespace caat {
+namespace host {
+
+bool attn_take_status(int* v) {
+  int w = 0, g = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(&w, g_status_word, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_status_word, &zero, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyFromSymbol(&g, g_arg_status, sizeof(int)) != cudaSuccess ||
+      cudaMemcpyToSymbol(g_arg_status, &zero, sizeof(int)) != cudaSuccess)
+    return false;
+  *v = w ? w : g;
+  return true;
+}
+
+}  // namespace host
+}  // namespace caat
+
+namespace {
+
+using caat::host::Recorder;
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a buffer, rows of a cache
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// A [P, T, heads, dh] operand: strides as given, or contiguous for (0, 0).
+struct View {
+  const caat_bf16* p = nullptr;
+  int64_t rank = 0, tok = 0;
+  uintptr_t lo = 0, hi = 0;  // bytes it spans
+};
+
+caat_status make_view(View* v, const caat_bf16* p, int64_t s_rank, int64_t s_tok, int P, int64_t T, int heads, int dh) {
+  v->p = p;
+  const int64_t row = int64_t(heads) * dh;
+  v->rank = s_rank;
+  v->tok = s_tok;
+  if (s_rank == 0 && s_tok == 0) {
+    v->tok = row;
+    v->rank = T * row;
+  }
+  if (!p) return CAAT_ERR_INVALID_ARG;
+  if (v->tok < row || v->rank < (P > 1 ? row : 0)) return CAAT_ERR_INVALID_ARG;
+  // a tensor map's strides are below 2^40 bytes; T tokens of 2^31 elements stay inside 64 bits
+  if (v->tok > (int64_t(1) << 31) || v->rank > (int64_t(1) << 38)) return CAAT_ERR_UNSUPPORTED;
+  if (v->tok % 8 != 0 || v->rank % 8 != 0 || !aligned16(p)) return CAAT_ERR_UNSUPPORTED;
+  v->lo = reinterpret_cast<uintptr_t>(p);
+  v->hi = v->lo + 2 * static_cast<uintptr_t>((P - 1) * v->rank + (T - 1) * v->tok + row);
+  return CAAT_OK;
+}
+
+struct Range {
+  uintptr_t lo, hi;
+};
+Range range_of(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, a + bytes};
+}
+bool meet(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
+Range range_of(const View& v) { return {v.lo, v.hi}; }
+
+caat::AttnView device_view(const View& v) { return {reinterpret_cast<const __nv_bfloat16*>(v.p), v.rank, v.tok}; }
+
+caat_status check_heads(int P, int hq, int hk, int dh, float scale) {
+  if (P < 1 || P > CAAT_MAX_P || hq < 1 || hk < 1 || dh < 1) return CAAT_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return CAAT_ERR_INVALID_ARG;
+  if (hq % hk != 0) return CAAT_ERR_INVALID_ARG;
+  if (dh % 8 != 0 || dh > 128 || hq > 1024) return CAAT_ERR_UNSUPPORTED;
+  return CAAT_OK;
+}
+
+caat_status check_offsets(const int32_t* cu, int n_seq, int64_t T) {
+  if (cu[0] < 0) return CAAT_ERR_INVALID_ARG;
+  for (int i = 0; i < n_seq; ++i)
+    if (cu[i + 1] < cu[i]) return CAAT_ERR_INVALID_ARG;
+  return cu[n_seq] <= T ? CAAT_OK : CAAT_ERR_INVALID_ARG;
+}
+
+}  // namespace
+
+extern "C" {
+
+caat_status caat_rope_frequencies(int rot, double theta, int scaling, double factor, double trained_length,
+                                  double* inv_freq, float* mscale_out) {
+  if (!inv_freq || rot < 2 || rot > 2 * caat::KR_MAX_PAIRS || rot % 2 != 0) return CAAT_ERR_INVALID_ARG;
+  if (!(theta > 1.0) || !std::isfinite(theta)) return CAAT_ERR_INVALID_ARG;
+  if (scaling < CAAT_ROPE_SCALING_NONE || scaling > CAAT_ROPE_SCALING_YARN) return CAAT_ERR_INVALID_ARG;
+  if (scaling != CAAT_ROPE_SCALING_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return CAAT_ERR_INVALID_ARG;
+  if (scaling == CAAT_ROPE_SCALING_NTK && rot < 4) return CAAT_ERR_INVALID_ARG;
+  if (scaling == CAAT_ROPE_SCALING_YARN && (!(trained_length > 0.0) || !std::isfinite(trained_length)))
+    return CAAT_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  if (scaling == CAAT_ROPE_SCALING_NTK) theta *= std::pow(factor, double(rot) / (rot - 2));
+  if (!std::isfinite(theta)) return CAAT_ERR_INVALID_ARG;
+  for (int j = 0; j < rot / 2; ++j) {
+    double f = std::pow(theta, -2.0 * j / rot);
+    if (scaling == CAAT_ROPE_SCALING_LINEAR) f /= factor;
+    if (scaling == CAAT_ROPE_SCALING_YARN) {
+      const double turns = trained_length * f / kTwoPi;
+      const double keep = std::min(1.0, std::max(0.0, (turns - 1.0) / (32.0 - 1.0)));
+      f *= keep + (1.0 - keep) / factor;
+    }
+    inv_freq[j] = f;
+  }
+  if (mscale_out) *mscale_out = scaling == CAAT_ROPE_SCALING_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return CAAT_OK;
+}
+
+caat_status caat_rope(const caat_rope_args* a) {
+  if (!a) return CAAT_ERR_INVALID_ARG;
+  if (a->P < 1 || a->P > CAAT_MAX_P || a->T < 0 || a->heads_q < 0 || a->heads_k < 0 || a->dh < 1 || a->rot < 1 ||
+      a->rot > a->dh || !std::isfinite(a->mscale))
+    return CAAT_ERR_INVALID_ARG;
+  if (a->flags & ~(CAAT_ROPE_FLAG_INTERLEAVED | CAAT_ROPE_FLAG_BACKWARD)) return CAAT_ERR_INVALID_ARG;
+  const bool inter = (a->flags & CAAT_ROPE_FLAG_INTERLEAVED) != 0;
+  if (a->dh % 8 != 0 || a->dh > 256 || a->rot % (inter ? 8 : 16) != 0) return CAAT_ERR_UNSUPPORTED;
+  if (a->T > kMaxRows || a->heads_q > 1024 || a->heads_k > 1024) return CAAT_ERR_UNSUPPORTED;
+  const bool append = a->slots != nullptr;
+  if (append && (a->cache_rows < 0 || a->heads_k == 0)) return CAAT_ERR_INVALID_ARG;
+  if (!a->inv_freq) return CAAT_ERR_INVALID_ARG;
+  for (int j = 0; j < a->rot / 2; ++j)
+    if (!std::isfinite(a->inv_freq[j])) return CAAT_ERR_INVALID_ARG;
+  if (a->T == 0 || (a->heads_q == 0 && a->heads_k == 0)) return CAAT_OK;
+
+  static thread_local caat::RopeParams prm;
+  std::memset(&prm, 0, sizeof(prm));
+  Range in[3], out[3];
+  int n_in = 0, n_out = 0;
+  auto tensor = [&](caat::RopeTensor* x, const caat_bf16* p, caat_bf16* o, int64_t s_rank, int64_t s_tok, int heads,
+                    bool to_cache) -> caat_status {
+    View v;
+    const caat_status s = make_view(&v, p, s_rank, s_tok, a->P, a->T, heads, a->dh);
+    if (s != CAAT_OK) return s;
+    if (!o) return CAAT_ERR_INVALID_ARG;
+    if (!aligned16(o)) return CAAT_ERR_UNSUPPORTED;
+    const int64_t row = int64_t(heads) * a->dh, rows = to_cache ? a->cache_rows : a->T;
+    const bool in_place = o == p && !to_cache;
+    x->in = reinterpret_cast<const __nv_bfloat16*>(p);
+    x->out = reinterpret_cast<__nv_bfloat16*>(o);
+    x->in_rank = v.rank;
+    x->in_tok = v.tok;
+    x->out_rank = in_place ? v.rank : rows * row;
+    x->out_tok = in_place ? v.tok : row;
+    x->heads = heads;
+    in[n_in++] = range_of(v);
+    if (!in_place) out[n_out++] = range_of(o, static_cast<size_t>(a->P) * rows * row * 2);
+    return CAAT_OK;
+  };
+  caat_status s = CAAT_OK;
+  if (a->heads_q) s = tensor(&prm.q, a->q, a->q_out, a->q_stride_rank, a->q_stride_token, a->heads_q, false);
+  if (s == CAAT_OK && a->heads_k)
+    s = tensor(&prm.k, a->k, a->k_out, a->k_stride_rank, a->k_stride_token, a->heads_k, append);
+  if (s == CAAT_OK && append) s = tensor(&prm.v, a->v, a->v_out, a->v_stride_rank, a->v_stride_token, a->heads_k, true);
+  if (s != CAAT_OK) return s;
+  if (append && a->cache_rows > (int64_t(1) << 40)) return CAAT_ERR_UNSUPPORTED;
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (meet(out[o], in[i])) return CAAT_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (meet(out[o], out[i])) return CAAT_ERR_INVALID_ARG;
+  }
+  if ((reinterpret_cast<uintptr_t>(a->positions) & 3u) || (reinterpret_cast<uintptr_t>(a->slots) & 7u))
+    return CAAT_ERR_UNSUPPORTED;
+  int sms = 0;
+  s = caat::host::device_sms(&sms);
+  if (s != CAAT_OK) return s;
+  prm.positions = a->positions;
+  prm.slots = a->slots;
+  prm.T = a->T;
+  prm.cache_rows = a->cache_rows;
+  prm.P = a->P;
+  prm.dh = a->dh;
+  prm.rot = a->rot;
+  prm.mscale = a->mscale;
+  constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
+  for (int j = 0; j < a->rot / 2; ++j)
+    prm.turns[j] = (a->flags & CAAT_ROPE_FLAG_BACKWARD ? -kInvTwoPi : kInvTwoPi) * a->inv_freq[j];
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  if (inter)
+    caat::rope_kernel<true><<<static_cast<unsigned>(a->T), caat::KR_THREADS, 0, a->stream>>>(prm);
+  else
+    caat::rope_kernel<false><<<static_cast<unsigned>(a->T), caat::KR_THREADS, 0, a->stream>>>(prm);
+  if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  rec.after_kernel(a->stream);
+  return CAAT_OK;
+}
+
+size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int heads_q, int heads_k, int dh,
+                                int variant) {
+  if (check_heads(P, heads_q, heads_k, dh, 1.f) != CAAT_OK || Tq < 0 || Tk < 0 || Tq > kMaxRows || Tk > kMaxRows)
+    return SIZE_MAX;
+  switch (variant) {
+    case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : 0;
+    case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : align256(size_t(P) * heads_q * Tq * 4);
+    case CAAT_VARIANT_ATTN_DECODE: return 0;
+  }
+  return SIZE_MAX;
+}
+
+caat_status caat_attn_forward(const caat_attn_args* a) {
+  if (!a) return CAAT_ERR_INVALID_ARG;
+  caat_status s = check_heads(a->P, a->heads_q, a->heads_k, a->dh, a->scale);
+  if (s != CAAT_OK) return s;
+  if (a->Tq < 0 || a->Tk < 0 || a->n_seq < 0 || a->flags != 0) return CAAT_ERR_INVALID_ARG;
+  if (a->Tq > kMaxRows || a->Tk > kMaxRows) return CAAT_ERR_UNSUPPORTED;
+  if (a->n_seq == 0 || a->Tq == 0) return CAAT_OK;
+  if (!a->cu_q) return CAAT_ERR_INVALID_ARG;
+  const int32_t* cu_k = a->cu_k ? a->cu_k : a->cu_q;
+  if ((s = check_offsets(a->cu_q, a->n_seq, a->Tq)) != CAAT_OK) return s;
+  if ((s = check_offsets(cu_k, a->n_seq, a->Tk)) != CAAT_OK) return s;
+  View q, k, v;
+  if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
+  if (a->Tk > 0) {
+    if ((s = make_view(&k, a->k, a->k_stride_rank, a->k_stride_token, a->P, a->Tk, a->heads_k, a->dh)) != CAAT_OK) return s;
+    if ((s = make_view(&v, a->v, a->v_stride_rank, a->v_stride_token, a->P, a->Tk, a->heads_k, a->dh)) != CAAT_OK) return s;
+  }
+  if (!a->out) return CAAT_ERR_INVALID_ARG;
+  if (!aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->lse) & 3u)) return CAAT_ERR_UNSUPPORTED;
+  const Range out = range_of(a->out, size_t(a->P) * a->Tq * a->heads_q * a->dh * 2);
+  const Range lse = range_of(a->lse, a->lse ? size_t(a->P) * a->Tq * a->heads_q * 4 : 0);
+  if (meet(lse, out) || meet(lse, range_of(q)) || meet(lse, range_of(k)) || meet(lse, range_of(v)))
+    return CAAT_ERR_INVALID_ARG;
+  if (meet(out, range_of(q)) || meet(out, range_of(k)) || meet(out, range_of(v))) return CAAT_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
+  caat::AttnSimple p{device_view(q), device_view(k), device_view(v), reinterpret_cast<__nv_bfloat16*>(a->out), a->lse,
+                     a->Tq, a->Tk, a->heads_q, a->heads_k, a->dh, a->scale};
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  for (int i = 0; i < a->n_seq; ++i) {
+    const int n = a->cu_q[i + 1] - a->cu_q[i], m = cu_k[i + 1] - cu_k[i];
+    if (n == 0) continue;
+    caat::attn_simple_kernel<<<dim3((n + 3) / 4, a->heads_q, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  }
+  rec.after_kernel(a->stream);
+  return CAAT_OK;
+}
+
+caat_status caat_attn_backward(const caat_attn_bwd_args* a) {
+  if (!a) return CAAT_ERR_INVALID_ARG;
+  caat_status s = check_heads(a->P, a->heads_q, a->heads_k, a->dh, a->scale);
+  if (s != CAAT_OK) return s;
+  if (a->Tq < 0 || a->Tk < 0 || a->n_seq < 0 || a->flags != 0) return CAAT_ERR_INVALID_ARG;
+  if (a->Tq > kMaxRows || a->Tk > kMaxRows) return CAAT_ERR_UNSUPPORTED;
+  if (a->n_seq == 0 || (a->Tq == 0 && a->Tk == 0)) return CAAT_OK;
+  if (!a->cu_q) return CAAT_ERR_INVALID_ARG;
+  const int32_t* cu_k = a->cu_k ? a->cu_k : a->cu_q;
+  if ((s = check_offsets(a->cu_q, a->n_seq, a->Tq)) != CAAT_OK) return s;
+  if ((s = check_offsets(cu_k, a->n_seq, a->Tk)) != CAAT_OK) return s;
+  View q, k, v;
+  Range in[5], out[3];
+  int n_in = 0, n_out = 0;
+  if (a->Tq > 0) {
+    if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
+    if (!a->out || !a->dout || !a->lse || !a->dq) return CAAT_ERR_INVALID_ARG;
+    if (!aligned16(a->out) || !aligned16(a->dout) || !aligned16(a->dq) || (reinterpret_cast<uintptr_t>(a->lse) & 3u))
+      return CAAT_ERR_UNSUPPORTED;
+    const size_t bytes = size_t(a->P) * a->Tq * a->heads_q * a->dh * 2;
+    in[n_in++] = range_of(q);
+    in[n_in++] = range_of(a->out, bytes);
+    in[n_in++] = range_of(a->dout, bytes);
+    out[n_out++] = range_of(a->dq, bytes);
+  }
+  if (a->Tk > 0) {
+    if ((s = make_view(&k, a->k, a->k_stride_rank, a->k_stride_token, a->P, a->Tk, a->heads_k, a->dh)) != CAAT_OK) return s;
+    if ((s = make_view(&v, a->v, a->v_stride_rank, a->v_stride_token, a->P, a->Tk, a->heads_k, a->dh)) != CAAT_OK) return s;
+    if (!a->dk || !a->dv) return CAAT_ERR_INVALID_ARG;
+    if (!aligned16(a->dk) || !aligned16(a->dv)) return CAAT_ERR_UNSUPPORTED;
+    const size_t bytes = size_t(a->P) * a->Tk * a->heads_k * a->dh * 2;
+    in[n_in++] = range_of(k);
+    in[n_in++] = range_of(v);
+    out[n_out++] = range_of(a->dk, bytes);
+    out[n_out++] = range_of(a->dv, bytes);
+  }
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (meet(out[o], in[i])) return CAAT_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (meet(out[o], out[i])) return CAAT_ERR_INVALID_ARG;
+  }
+  const size_t need =
+      caat_attn_workspace_size(a->Tq, a->Tk, a->n_seq, a->P, a->heads_q, a->heads_k, a->dh, CAAT_VARIANT_ATTN_BWD);
+  if (need > 0 && (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)))
+    return CAAT_ERR_WORKSPACE;
+  int sms = 0;
+  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
+  caat::AttnSimpleBwd p{};
+  p.f = {device_view(q), device_view(k), device_view(v),
+         const_cast<__nv_bfloat16*>(reinterpret_cast<const __nv_bfloat16*>(a->out)), const_cast<float*>(a->lse),
+         a->Tq, a->Tk, a->heads_q, a->heads_k, a->dh, a->scale};
+  p.dout = reinterpret_cast<const __nv_bfloat16*>(a->dout);
+  p.dq = reinterpret_cast<__nv_bfloat16*>(a->dq);
+  p.dk = reinterpret_cast<__nv_bfloat16*>(a->dk);
+  p.dv = reinterpret_cast<__nv_bfloat16*>(a->dv);
+  p.D = static_cast<float*>(a->workspace);
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  for (int i = 0; i < a->n_seq; ++i) {
+    const int n = a->cu_q[i + 1] - a->cu_q[i], m = cu_k[i + 1] - cu_k[i];
+    if (n > 0)
+      caat::attn_simple_dq_kernel<<<dim3((n + 3) / 4, a->heads_q, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
+    if (m > 0)
+      caat::attn_simple_dkv_kernel<<<dim3((m + 3) / 4, a->heads_k, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  }
+  rec.after_kernel(a->stream);
+  return CAAT_OK;
+}
+
+caat_status caat_attn_decode(const caat_attn_decode_args* a) {
+  if (!a) return CAAT_ERR_INVALID_ARG;
+  caat_status s = check_heads(a->P, a->heads_q, a->heads_k, a->dh, a->scale);
+  if (s != CAAT_OK) return s;
+  if (a->B < 0 || a->capacity < 0 || a->flags != 0) return CAAT_ERR_INVALID_ARG;
+  if (a->capacity > kMaxRows || a->B > 65535) return CAAT_ERR_UNSUPPORTED;
+  if (a->B == 0) return CAAT_OK;
+  View q;
+  if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->B, a->heads_q, a->dh)) != CAAT_OK) return s;
+  if (!a->lens || !a->out || (a->capacity > 0 && (!a->k_cache || !a->v_cache))) return CAAT_ERR_INVALID_ARG;
+  if (!aligned16(a->k_cache) || !aligned16(a->v_cache) || !aligned16(a->out) || (reinterpret_cast<uintptr_t>(a->lens) & 3u))
+    return CAAT_ERR_UNSUPPORTED;
+  const Range out = range_of(a->out, size_t(a->P) * a->B * a->heads_q * a->dh * 2);
+  const size_t cache = size_t(a->P) * a->B * a->capacity * a->heads_k * a->dh * 2;
+  if (meet(out, range_of(q)) || meet(out, range_of(a->k_cache, cache)) || meet(out, range_of(a->v_cache, cache)) ||
+      meet(out, range_of(a->lens, size_t(a->B) * 4)))
+    return CAAT_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
+  caat::AttnSimpleDecode p{device_view(q), reinterpret_cast<const __nv_bfloat16*>(a->k_cache),
+                           reinterpret_cast<const __nv_bfloat16*>(a->v_cache), a->lens,
+                           reinterpret_cast<__nv_bfloat16*>(a->out), a->B, a->capacity, a->heads_q, a->heads_k, a->dh,
+                           a->scale};
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  caat::attn_simple_decode_kernel<<<dim3(static_cast<unsigned>(a->B), a->heads_q, a->P), 32, 0, a->stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  rec.after_kernel(a->stream);
+  return CAAT_OK;
+}
+
+}  // extern "C"

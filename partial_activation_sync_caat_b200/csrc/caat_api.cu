@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "caat.h"
+#include "host_common.h"
 #include "ptx.cuh"
 #include "rowpar_gemm.cuh"
 #include "rowpar_gemm2.cuh"
@@ -326,9 +327,7 @@ uint64_t timeout_ns() {
 // ---------------------------------------------------------------------------------------
 // Tensor maps (driver entry point fetched through the runtime; no link to libcuda)
 // ---------------------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using caat::host::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = [] {
@@ -629,40 +628,9 @@ MlpWs mlp_ws_layout(int64_t T, int64_t H, int64_t F, int P, bool fused) {
 
 }  // namespace
 
-// ---------------------------------------------------------------------------------------
-// Timing recorder
-// ---------------------------------------------------------------------------------------
-struct caat_timing {
-  int capacity = 0;
-  int max_kernels = 8;
-  int n = 0;
-  std::vector<cudaEvent_t> ev;
-  std::vector<int> nk;
-};
-
 namespace {
 
-struct Recorder {
-  caat_timing* t = nullptr;
-  int rec = -1;
-  int k = 0;
-  void begin(caat_timing* tm, cudaStream_t s) {
-    t = tm;
-    if (!t || t->n >= t->capacity) {
-      t = nullptr;
-      return;
-    }
-    rec = t->n++;
-    k = 0;
-    cudaEventRecord(t->ev[rec * (t->max_kernels + 1)], s);
-  }
-  void after_kernel(cudaStream_t s) {
-    if (!t || k >= t->max_kernels) return;
-    ++k;
-    cudaEventRecord(t->ev[rec * (t->max_kernels + 1) + k], s);
-    t->nk[rec] = k;
-  }
-};
+using caat::host::Recorder;
 
 // ---------------------------------------------------------------------------------------
 // The row-parallel layer: GEMM + partial channel-reduce + residual (K1), RMSNorm (K2)
@@ -1241,6 +1209,26 @@ caat_status launch_batched_gemm(const void* A, const void* B, void* Cm, int nb, 
 // =======================================================================================
 // C ABI
 // =======================================================================================
+// Shared with attn_api.cu (host_common.h).
+namespace caat {
+namespace host {
+
+caat_status device_sms(int* sm_count) {
+  DeviceInfo* d = nullptr;
+  const caat_status s = device_info(&d);
+  if (s == CAAT_OK) *sm_count = d->sm_count;
+  return s;
+}
+
+CUcontext context() { return current_context(); }
+
+uint64_t wait_limit_ns() { return timeout_ns(); }
+
+EncodeTiledFn tensor_map_encoder() { return encode_fn(); }
+
+}  // namespace host
+}  // namespace caat
+
 extern "C" {
 
 const char* caat_status_string(caat_status s) {
@@ -2027,6 +2015,9 @@ caat_status caat_get_device_status(caat_stream_t stream, int32_t* status_out) {
   if (cudaMemcpyFromSymbol(&v, caat::g_status_word, sizeof(int)) != cudaSuccess) return CAAT_ERR_CUDA;
   const int zero = 0;
   if (cudaMemcpyToSymbol(caat::g_status_word, &zero, sizeof(int)) != cudaSuccess) return CAAT_ERR_CUDA;
+  int w = 0;
+  if (!caat::host::attn_take_status(&w)) return CAAT_ERR_CUDA;
+  if (v == 0) v = w;
   *status_out = v;
   return (v & 0xFF) == 0 ? CAAT_OK : static_cast<caat_status>(v & 0xFF);
 }
