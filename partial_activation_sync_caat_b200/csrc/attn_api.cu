@@ -7,11 +7,14 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
+#include <new>
 #include <vector>
 
 #include "caat.h"
 #include "host_common.h"
 #include "ptx.cuh"
+#include "attn_fwd.cuh"
 #include "attn_simple.cuh"
 #include "rope.cuh"
 
@@ -93,6 +96,120 @@ caat_status check_offsets(const int32_t* cu, int n_seq, int64_t T) {
   for (int i = 0; i < n_seq; ++i)
     if (cu[i + 1] < cu[i]) return CAAT_ERR_INVALID_ARG;
   return cu[n_seq] <= T ? CAAT_OK : CAAT_ERR_INVALID_ARG;
+}
+
+// One-time kernel attributes, per device and context.
+caat_status attn_setup(int* sms) {
+  const caat_status s = caat::host::device_sms(sms);
+  if (s != CAAT_OK) return s;
+  static std::mutex mu;
+  static CUcontext done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CAAT_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(mu);
+  const CUcontext ctx = caat::host::context();
+  if (done[dev] == ctx && ctx) return CAAT_OK;
+  auto smem = [](auto* kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  if (!smem(caat::attn_fwd_kernel<64>, caat::FwdCfg<64>::kSmem) || !smem(caat::attn_fwd_kernel<128>, caat::FwdCfg<128>::kSmem))
+    return CAAT_ERR_CUDA;
+  done[dev] = ctx;
+  return CAAT_OK;
+}
+
+// Tensor map of a [P, T, heads, dh] operand as (dh, heads, T, P) in boxes of 64 elements x 128 tokens
+// of one head, 128-byte swizzle; elements past dh and tokens past T read as zeros.
+caat_status heads_map(CUtensorMap* map, const View& v, int P, int64_t T, int heads, int dh) {
+  const caat::host::EncodeTiledFn fn = caat::host::tensor_map_encoder();
+  if (!fn) return CAAT_ERR_CUDA;
+  const cuuint64_t dims[4] = {cuuint64_t(dh), cuuint64_t(heads), cuuint64_t(T), cuuint64_t(P)};
+  const int64_t rank = P > 1 ? v.rank : v.tok;  // one rank: never stepped over
+  const cuuint64_t strides[3] = {cuuint64_t(dh) * 2, cuuint64_t(v.tok) * 2, cuuint64_t(rank) * 2};
+  const cuuint32_t box[4] = {64, 1, caat::KA_TILE, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<caat_bf16*>(v.p), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CAAT_OK : CAAT_ERR_CUDA;
+}
+
+// Most entries a work list of `step` rows each can have.
+int64_t max_jobs(int64_t T, int n_seq, int step) { return T / step + n_seq; }
+
+size_t list_bytes(int64_t jobs) { return jobs <= caat::KA_INLINE_JOBS ? 0 : align256(size_t(jobs) * sizeof(caat::AttnJob)); }
+
+// Queries of each sequence cut into jobs of `step` rows, those with the most keys first: the last jobs
+// to start are then the shortest, which evens out when the SMs run dry.
+void query_jobs(const int32_t* cu_q, const int32_t* cu_k, int n_seq, int step, std::vector<caat::AttnJob>& jobs) {
+  jobs.clear();
+  for (int s = 0; s < n_seq; ++s) {
+    const int n = cu_q[s + 1] - cu_q[s], m = cu_k[s + 1] - cu_k[s];
+    for (int i = 0; i < n; i += step) jobs.push_back({cu_q[s] + i, std::min(step, n - i), cu_k[s], i + 1 + (m - n)});
+  }
+  std::stable_sort(jobs.begin(), jobs.end(),
+                   [](const caat::AttnJob& a, const caat::AttnJob& b) { return a.first + a.rows > b.first + b.rows; });
+}
+
+// The list into the launch's arguments, or through `dst` in the workspace (queued on the stream).
+caat_status place_jobs(const std::vector<caat::AttnJob>& jobs, caat::AttnJobList* list, void* dst, cudaStream_t st) {
+  if (jobs.size() <= size_t(caat::KA_INLINE_JOBS)) {
+    list->far = nullptr;
+    std::copy(jobs.begin(), jobs.end(), list->near);
+    return CAAT_OK;
+  }
+  caat::AttnJob* far = static_cast<caat::AttnJob*>(dst);
+  list->far = far;
+  static thread_local caat::AttnJobChunk chunk;
+  for (size_t i = 0; i < jobs.size(); i += caat::KA_UPLOAD_JOBS) {
+    const size_t n = std::min(jobs.size() - i, size_t(caat::KA_UPLOAD_JOBS));
+    std::copy(jobs.begin() + i, jobs.begin() + i + n, chunk.job);
+    caat::attn_upload_kernel<<<1, caat::KA_UPLOAD_JOBS, 0, st>>>(far + i, static_cast<int>(n), chunk);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  }
+  return CAAT_OK;
+}
+
+caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, const View& q, const View& k, const View& v) {
+  int sms = 0;
+  caat_status s = attn_setup(&sms);
+  if (s != CAAT_OK) return s;
+  const int group = a->heads_q / a->heads_k;
+  static thread_local std::vector<caat::AttnJob> jobs;
+  static thread_local caat::FwdParams prm;
+  // Two heads of a group on the same 128 rows when the group is even: both tiles then need the same
+  // key blocks, and a short sequence wastes less than with 256 rows of one head.
+  prm.pair_heads = group % 2 == 0 ? 1 : 0;
+  query_jobs(a->cu_q, cu_k, a->n_seq, prm.pair_heads ? caat::KA_TILE : 2 * caat::KA_TILE, jobs);
+  if (jobs.empty()) return CAAT_OK;
+  prm.out = reinterpret_cast<__nv_bfloat16*>(a->out);
+  prm.lse = a->lse;
+  prm.Tq = a->Tq;
+  prm.hq = a->heads_q;
+  prm.hk = a->heads_k;
+  prm.dh = a->dh;
+  prm.group = group;
+  prm.n_heads = prm.pair_heads ? a->heads_q / 2 : a->heads_q;
+  prm.per_job = a->P * prm.n_heads;
+  prm.scale = a->scale;
+  prm.timeout_ns = caat::host::wait_limit_ns();
+  const int64_t grid = int64_t(jobs.size()) * prm.per_job;
+  if (grid > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
+  CUtensorMap mq, mk, mv;
+  if ((s = heads_map(&mq, q, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
+  // no keys at all: every row is empty and neither map is used
+  if ((s = heads_map(&mk, a->Tk ? k : q, a->P, a->Tk ? a->Tk : 1, a->Tk ? a->heads_k : 1, a->dh)) != CAAT_OK) return s;
+  if ((s = heads_map(&mv, a->Tk ? v : q, a->P, a->Tk ? a->Tk : 1, a->Tk ? a->heads_k : 1, a->dh)) != CAAT_OK) return s;
+  if ((s = place_jobs(jobs, &prm.jobs, a->workspace, a->stream)) != CAAT_OK) return s;
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  if (a->dh <= 64)
+    caat::attn_fwd_kernel<64><<<static_cast<unsigned>(grid), caat::KF_THREADS, caat::FwdCfg<64>::kSmem, a->stream>>>(mq, mk, mv, prm);
+  else
+    caat::attn_fwd_kernel<128><<<static_cast<unsigned>(grid), caat::KF_THREADS, caat::FwdCfg<128>::kSmem, a->stream>>>(mq, mk, mv, prm);
+  if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  rec.after_kernel(a->stream);
+  return CAAT_OK;
 }
 
 }  // namespace
@@ -210,7 +327,7 @@ size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int he
   if (check_heads(P, heads_q, heads_k, dh, 1.f) != CAAT_OK || Tq < 0 || Tk < 0 || Tq > kMaxRows || Tk > kMaxRows)
     return SIZE_MAX;
   switch (variant) {
-    case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : 0;
+    case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
     case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : align256(size_t(P) * heads_q * Tq * 4);
     case CAAT_VARIANT_ATTN_DECODE: return 0;
   }
@@ -241,20 +358,14 @@ caat_status caat_attn_forward(const caat_attn_args* a) {
   if (meet(lse, out) || meet(lse, range_of(q)) || meet(lse, range_of(k)) || meet(lse, range_of(v)))
     return CAAT_ERR_INVALID_ARG;
   if (meet(out, range_of(q)) || meet(out, range_of(k)) || meet(out, range_of(v))) return CAAT_ERR_INVALID_ARG;
-  int sms = 0;
-  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
-  caat::AttnSimple p{device_view(q), device_view(k), device_view(v), reinterpret_cast<__nv_bfloat16*>(a->out), a->lse,
-                     a->Tq, a->Tk, a->heads_q, a->heads_k, a->dh, a->scale};
-  Recorder rec;
-  rec.begin(a->timing, a->stream);
-  for (int i = 0; i < a->n_seq; ++i) {
-    const int n = a->cu_q[i + 1] - a->cu_q[i], m = cu_k[i + 1] - cu_k[i];
-    if (n == 0) continue;
-    caat::attn_simple_kernel<<<dim3((n + 3) / 4, a->heads_q, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
-    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  const size_t need = caat_attn_workspace_size(a->Tq, a->Tk, a->n_seq, a->P, a->heads_q, a->heads_k, a->dh, CAAT_VARIANT_ATTN);
+  if (need > 0 && (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)))
+    return CAAT_ERR_WORKSPACE;
+  try {
+    return launch_attn_forward(a, cu_k, q, k, v);
+  } catch (const std::bad_alloc&) {
+    return CAAT_ERR_CUDA;
   }
-  rec.after_kernel(a->stream);
-  return CAAT_OK;
 }
 
 caat_status caat_attn_backward(const caat_attn_bwd_args* a) {

@@ -47,30 +47,6 @@ __device__ __forceinline__ void axpy4(float4& o, float a, float4 x) {
   o.w = fmaf(a, x.w, o.w);
 }
 
-// One sequence: queries [q0, q0 + n), keys [k0, k0 + m).
-__global__ void __launch_bounds__(128) attn_simple_kernel(AttnSimple a, int q0, int n, int k0, int m) {
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, e = 4 * lane;
-  if (i >= n) return;
-  const int h = blockIdx.y, r = blockIdx.z, kv = h / (a.hq / a.hk);
-  const int64_t row = q0 + i;
-  const float4 q = ld_row4(a.q.p + r * a.q.rank + row * a.q.tok + h * a.dh, e, a.dh);
-  const int seen = i + 1 + (m - n);
-  float top = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < seen; ++j) {
-    const float s = a.scale * warp_dot4(q, ld_row4(a.k.p + r * a.k.rank + int64_t(k0 + j) * a.k.tok + kv * a.dh, e, a.dh));
-    const float t = fmaxf(top, s);
-    const float c = top == -INFINITY ? 0.f : expf(top - t), p = expf(s - t);
-    sum = sum * c + p;
-    o = make_float4(o.x * c, o.y * c, o.z * c, o.w * c);
-    axpy4(o, p, ld_row4(a.v.p + r * a.v.rank + int64_t(k0 + j) * a.v.tok + kv * a.dh, e, a.dh));
-    top = t;
-  }
-  const float inv = seen > 0 ? 1.f / sum : 0.f;
-  st_row4(a.out + ((r * a.Tq + row) * a.hq + h) * a.dh, e, a.dh, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (a.lse && lane == 0) a.lse[(int64_t(r) * a.hq + h) * a.Tq + row] = seen > 0 ? top + logf(sum) : -INFINITY;
-}
-
 struct AttnSimpleBwd {
   AttnSimple f;
   const __nv_bfloat16* dout;
