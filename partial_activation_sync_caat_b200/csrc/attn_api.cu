@@ -14,6 +14,7 @@
 #include "caat.h"
 #include "host_common.h"
 #include "ptx.cuh"
+#include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
 #include "attn_simple.cuh"
 #include "rope.cuh"
@@ -112,21 +113,23 @@ caat_status attn_setup(int* sms) {
   auto smem = [](auto* kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
   };
-  if (!smem(caat::attn_fwd_kernel<64>, caat::FwdCfg<64>::kSmem) || !smem(caat::attn_fwd_kernel<128>, caat::FwdCfg<128>::kSmem))
+  if (!smem(caat::attn_fwd_kernel<64>, caat::FwdCfg<64>::kSmem) || !smem(caat::attn_fwd_kernel<128>, caat::FwdCfg<128>::kSmem) ||
+      !smem(caat::attn_dq_kernel<64>, caat::DqCfg<64>::kSmem) || !smem(caat::attn_dq_kernel<128>, caat::DqCfg<128>::kSmem) ||
+      !smem(caat::attn_dkv_kernel<64>, caat::DkvCfg<64>::kSmem) || !smem(caat::attn_dkv_kernel<128>, caat::DkvCfg<128>::kSmem))
     return CAAT_ERR_CUDA;
   done[dev] = ctx;
   return CAAT_OK;
 }
 
-// Tensor map of a [P, T, heads, dh] operand as (dh, heads, T, P) in boxes of 64 elements x 128 tokens
-// of one head, 128-byte swizzle; elements past dh and tokens past T read as zeros.
-caat_status heads_map(CUtensorMap* map, const View& v, int P, int64_t T, int heads, int dh) {
+// Tensor map of a [P, T, heads, dh] operand as (dh, heads, T, P) in boxes of 64 elements x box_rows
+// tokens of one head, 128-byte swizzle; elements past dh and tokens past T read as zeros.
+caat_status heads_map(CUtensorMap* map, const View& v, int P, int64_t T, int heads, int dh, int box_rows = caat::KA_TILE) {
   const caat::host::EncodeTiledFn fn = caat::host::tensor_map_encoder();
   if (!fn) return CAAT_ERR_CUDA;
   const cuuint64_t dims[4] = {cuuint64_t(dh), cuuint64_t(heads), cuuint64_t(T), cuuint64_t(P)};
   const int64_t rank = P > 1 ? v.rank : v.tok;  // one rank: never stepped over
   const cuuint64_t strides[3] = {cuuint64_t(dh) * 2, cuuint64_t(v.tok) * 2, cuuint64_t(rank) * 2};
-  const cuuint32_t box[4] = {64, 1, caat::KA_TILE, 1};
+  const cuuint32_t box[4] = {64, 1, cuuint32_t(box_rows), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<caat_bf16*>(v.p), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -145,10 +148,47 @@ void query_jobs(const int32_t* cu_q, const int32_t* cu_k, int n_seq, int step, s
   jobs.clear();
   for (int s = 0; s < n_seq; ++s) {
     const int n = cu_q[s + 1] - cu_q[s], m = cu_k[s + 1] - cu_k[s];
-    for (int i = 0; i < n; i += step) jobs.push_back({cu_q[s] + i, std::min(step, n - i), cu_k[s], i + 1 + (m - n)});
+    for (int i = 0; i < n; i += step) jobs.push_back({cu_q[s] + i, std::min(step, n - i), cu_k[s], i + 1 + (m - n), 0});
   }
   std::stable_sort(jobs.begin(), jobs.end(),
                    [](const caat::AttnJob& a, const caat::AttnJob& b) { return a.first + a.rows > b.first + b.rows; });
+}
+
+// Keys of each sequence in tiles of 128, each with the queries that see any of them, most first.
+void key_jobs(const int32_t* cu_q, const int32_t* cu_k, int n_seq, std::vector<caat::AttnJob>& jobs) {
+  jobs.clear();
+  for (int s = 0; s < n_seq; ++s) {
+    const int n = cu_q[s + 1] - cu_q[s], m = cu_k[s + 1] - cu_k[s];
+    for (int j = 0; j < m; j += caat::KA_TILE) {
+      const int sees = j - (m - n);  // the first query that sees key j, if not before the sequence's first
+      const int i0 = std::min(std::max(sees, 0), n);
+      jobs.push_back({cu_q[s] + i0, n - i0, cu_k[s] + j, sees - i0, std::min(caat::KA_TILE, m - j)});
+    }
+  }
+  std::stable_sort(jobs.begin(), jobs.end(), [](const caat::AttnJob& a, const caat::AttnJob& b) { return a.rows > b.rows; });
+}
+
+// CTAs that share the queries of a key tile (their fp32 sums are then joined by another kernel): enough
+// for two waves of the 148 SMs when ranks, key heads and tiles alone do not give them.
+int dkv_splits(int64_t Tk, int P, int hk) {
+  const int64_t units = std::max<int64_t>(Tk / caat::KA_TILE, 1) * P * hk;
+  return static_cast<int>(std::min<int64_t>(16, (2 * 148 + units - 1) / units));
+}
+
+struct BwdLayout {
+  size_t D, q_list, k_list, part, total;
+  int splits;
+};
+
+BwdLayout bwd_layout(int64_t Tq, int64_t Tk, int n_seq, int P, int hq, int hk, int dh) {
+  BwdLayout L{};
+  L.splits = dkv_splits(Tk, P, hk);
+  L.D = 0;
+  L.q_list = align256(size_t(P) * hq * Tq * 4);
+  L.k_list = L.q_list + list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
+  L.part = L.k_list + list_bytes(max_jobs(Tk, n_seq, caat::KA_TILE));
+  L.total = L.part + (L.splits > 1 ? align256(size_t(2) * L.splits * P * Tk * hk * dh * 4) : 0);
+  return L;
 }
 
 // The list into the launch's arguments, or through `dst` in the workspace (queued on the stream).
@@ -209,6 +249,85 @@ caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, co
     caat::attn_fwd_kernel<128><<<static_cast<unsigned>(grid), caat::KF_THREADS, caat::FwdCfg<128>::kSmem, a->stream>>>(mq, mk, mv, prm);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
+  return CAAT_OK;
+}
+
+caat_status launch_attn_backward(const caat_attn_bwd_args* a, const int32_t* cu_k, const View& q, const View& k, const View& v) {
+  int sms = 0;
+  caat_status s = attn_setup(&sms);
+  if (s != CAAT_OK) return s;
+  const int P = a->P, hq = a->heads_q, hk = a->heads_k, dh = a->dh;
+  const BwdLayout L = bwd_layout(a->Tq, a->Tk, a->n_seq, P, hq, hk, dh);
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  static thread_local std::vector<caat::AttnJob> jobs;
+  static thread_local caat::BwdAttnParams prm;
+  prm.out = reinterpret_cast<const __nv_bfloat16*>(a->out);
+  prm.dout = reinterpret_cast<const __nv_bfloat16*>(a->dout);
+  prm.lse = a->lse;
+  prm.D = reinterpret_cast<float*>(ws + L.D);
+  prm.dq = reinterpret_cast<__nv_bfloat16*>(a->dq);
+  prm.dk = reinterpret_cast<__nv_bfloat16*>(a->dk);
+  prm.dv = reinterpret_cast<__nv_bfloat16*>(a->dv);
+  prm.part = reinterpret_cast<float*>(ws + L.part);
+  prm.Tq = a->Tq;
+  prm.Tk = a->Tk;
+  prm.P = P;
+  prm.hq = hq;
+  prm.hk = hk;
+  prm.dh = dh;
+  prm.group = hq / hk;
+  prm.splits = L.splits;
+  prm.scale = a->scale;
+  prm.timeout_ns = caat::host::wait_limit_ns();
+  const View& any = a->Tq ? q : k;  // a side without rows is never read
+  View g = any;
+  if (a->Tq) {
+    g.p = a->dout;
+    g.tok = int64_t(hq) * dh;
+    g.rank = a->Tq * g.tok;
+  }
+  const int64_t Tq = a->Tq ? a->Tq : 1, Tk = a->Tk ? a->Tk : 1;
+  const int hq_m = a->Tq ? hq : 1, hk_m = a->Tk ? hk : 1;
+  CUtensorMap mq, mg, mk, mv, mq64, mg64;
+  if ((s = heads_map(&mq, any, P, Tq, hq_m, dh)) != CAAT_OK || (s = heads_map(&mg, g, P, Tq, hq_m, dh)) != CAAT_OK ||
+      (s = heads_map(&mk, a->Tk ? k : any, P, Tk, hk_m, dh)) != CAAT_OK ||
+      (s = heads_map(&mv, a->Tk ? v : any, P, Tk, hk_m, dh)) != CAAT_OK ||
+      (s = heads_map(&mq64, any, P, Tq, hq_m, dh, caat::KB2_QT)) != CAAT_OK ||
+      (s = heads_map(&mg64, g, P, Tq, hq_m, dh, caat::KB2_QT)) != CAAT_OK)
+    return s;
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  query_jobs(a->cu_q, cu_k, a->n_seq, caat::KA_TILE, jobs);
+  if (!jobs.empty()) {
+    prm.per_job = P * hq;
+    const int64_t grid = int64_t(jobs.size()) * prm.per_job;
+    if (grid > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
+    if ((s = place_jobs(jobs, &prm.jobs, ws + L.q_list, a->stream)) != CAAT_OK) return s;
+    if (dh <= 64)
+      caat::attn_dq_kernel<64><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DqCfg<64>::kSmem, a->stream>>>(mq, mg, mk, mv, prm);
+    else
+      caat::attn_dq_kernel<128><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DqCfg<128>::kSmem, a->stream>>>(mq, mg, mk, mv, prm);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    rec.after_kernel(a->stream);
+  }
+  key_jobs(a->cu_q, cu_k, a->n_seq, jobs);
+  if (!jobs.empty()) {
+    prm.per_job = P * hk * L.splits;
+    const int64_t grid = int64_t(jobs.size()) * prm.per_job;
+    if (grid > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
+    if ((s = place_jobs(jobs, &prm.jobs, ws + L.k_list, a->stream)) != CAAT_OK) return s;
+    if (dh <= 64)
+      caat::attn_dkv_kernel<64><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DkvCfg<64>::kSmem, a->stream>>>(mq64, mg64, mk, mv, prm);
+    else
+      caat::attn_dkv_kernel<128><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DkvCfg<128>::kSmem, a->stream>>>(mq64, mg64, mk, mv, prm);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    rec.after_kernel(a->stream);
+    if (L.splits > 1) {
+      caat::attn_dkv_join_kernel<<<dim3(static_cast<unsigned>(jobs.size()), P, 4), 256, 0, a->stream>>>(prm);
+      if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+      rec.after_kernel(a->stream);
+    }
+  }
   return CAAT_OK;
 }
 
@@ -328,7 +447,7 @@ size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int he
     return SIZE_MAX;
   switch (variant) {
     case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
-    case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : align256(size_t(P) * heads_q * Tq * 4);
+    case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : bwd_layout(Tq, Tk, n_seq, P, heads_q, heads_k, dh).total;
     case CAAT_VARIANT_ATTN_DECODE: return 0;
   }
   return SIZE_MAX;
@@ -414,29 +533,11 @@ caat_status caat_attn_backward(const caat_attn_bwd_args* a) {
       caat_attn_workspace_size(a->Tq, a->Tk, a->n_seq, a->P, a->heads_q, a->heads_k, a->dh, CAAT_VARIANT_ATTN_BWD);
   if (need > 0 && (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)))
     return CAAT_ERR_WORKSPACE;
-  int sms = 0;
-  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
-  caat::AttnSimpleBwd p{};
-  p.f = {device_view(q), device_view(k), device_view(v),
-         const_cast<__nv_bfloat16*>(reinterpret_cast<const __nv_bfloat16*>(a->out)), const_cast<float*>(a->lse),
-         a->Tq, a->Tk, a->heads_q, a->heads_k, a->dh, a->scale};
-  p.dout = reinterpret_cast<const __nv_bfloat16*>(a->dout);
-  p.dq = reinterpret_cast<__nv_bfloat16*>(a->dq);
-  p.dk = reinterpret_cast<__nv_bfloat16*>(a->dk);
-  p.dv = reinterpret_cast<__nv_bfloat16*>(a->dv);
-  p.D = static_cast<float*>(a->workspace);
-  Recorder rec;
-  rec.begin(a->timing, a->stream);
-  for (int i = 0; i < a->n_seq; ++i) {
-    const int n = a->cu_q[i + 1] - a->cu_q[i], m = cu_k[i + 1] - cu_k[i];
-    if (n > 0)
-      caat::attn_simple_dq_kernel<<<dim3((n + 3) / 4, a->heads_q, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
-    if (m > 0)
-      caat::attn_simple_dkv_kernel<<<dim3((m + 3) / 4, a->heads_k, a->P), 128, 0, a->stream>>>(p, a->cu_q[i], n, cu_k[i], m);
-    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  try {
+    return launch_attn_backward(a, cu_k, q, k, v);
+  } catch (const std::bad_alloc&) {
+    return CAAT_ERR_CUDA;
   }
-  rec.after_kernel(a->stream);
-  return CAAT_OK;
 }
 
 caat_status caat_attn_decode(const caat_attn_decode_args* a) {

@@ -1,0 +1,632 @@
+// attn_bwd.cuh - gradients of the packed causal attention on the tensor cores.
+//
+//   p_ij = 2^(c s_ij - lse_i log2(e)),  dP = dO V^T,  D_i = sum_d dO_id O_id,  dS = p (dP - D)
+//   dQ = scale dS K,   dV = p^T dO,   dK = scale dS^T Q
+//
+// Two kernels, so that every sum has one owner and a fixed order (one kernel that walks the scores
+// once would have to add dQ into memory from every key block, in an order that changes from run to
+// run): dq walks the keys of a query tile and also leaves D for the second; dkv walks the queries of
+// a key tile.  The scores and dP are computed in both: 7 products of 128 x 128 x dh per pair of
+// tiles instead of 5.
+//
+// p and dS are rounded to bf16 to be operands of the products (their A operand, read from tensor
+// memory); the scale is applied once to the fp32 sums.  Masked scores are replaced, never added to;
+// operand rows of another sequence that meet p = 0 or dS = 0 in a product are zeroed in shared memory
+// first, since 0 times a NaN or an infinity is NaN.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace caat {
+
+constexpr int KB2_THREADS = 384;  // warps 0-7: elementwise, 8: MMA, 9: TMA, 10: scrubbing, 11: idle
+constexpr int KB2_QT = 64;        // queries per step of the dkv kernel
+
+struct BwdAttnParams {
+  const __nv_bfloat16* out;   // [P, Tq, hq, dh]
+  const __nv_bfloat16* dout;
+  const float* lse;           // [P, hq, Tq]
+  float* D;                   // [P, hq, Tq]
+  __nv_bfloat16 *dq, *dk, *dv;
+  float* part;                // [2][splits][P, Tk, hk, dh] partial dk, dv (splits > 1)
+  int64_t Tq, Tk;
+  int P, hq, hk, dh, group;
+  int per_job;                // grid units per job
+  int splits;                 // CTAs that share the queries of a key tile
+  float scale;
+  uint64_t timeout_ns;
+  AttnJobList jobs;
+};
+
+template <int HD>
+struct DqCfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * KA_BOX_BYTES;
+  // A K block is held until the product with dS, one block longer than its V block.
+  static constexpr int kK = HD == 128 ? 3 : 4;
+  static constexpr int kV = HD == 128 ? 2 : 3;
+  static constexpr int kSlots = kK + kV;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + 2 * KA_TILE * 4 + 512;
+  static __device__ __forceinline__ int k_slot(int j) { return j % kK; }
+  static __device__ __forceinline__ int v_slot(int j) { return kK + j % kV; }
+};
+
+// One CTA: 128 queries of one head.  Tensor memory: S | dP | dQ | dS of even blocks | of odd blocks.
+// All 8 elementwise warps work on one block at a time (a thread has one row and 64 of the 128 keys);
+// they copy S and dP to registers and free them at once, so that the next block's two products run
+// meanwhile, and the product with K follows when dS is written.
+template <int HD>
+__global__ void __launch_bounds__(KB2_THREADS, 1)
+    attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ BwdAttnParams prm) {
+  using Cfg = DqCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sQ = smem;
+  uint8_t* sG = smem + Cfg::kTileBytes;
+  uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
+  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 2 * KA_TILE);
+  uint64_t* q_full = bars;
+  uint64_t* full = q_full + 1;             // [slots]
+  uint64_t* empty = full + Cfg::kSlots;    // [slots]
+  uint64_t* sd_full = empty + Cfg::kSlots;
+  uint64_t* sd_free = sd_full + 1;         // 8 warps
+  uint64_t* ds_full = sd_free + 1;         // 8 warps
+  uint64_t* k_raw = ds_full + 1;           // the last key block has arrived, to be scrubbed
+  uint64_t* scrubbed = k_raw + 1;
+  uint64_t* dq_done = scrubbed + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dq_done + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int ji = blockIdx.x / prm.per_job;
+  const int rh = blockIdx.x - ji * prm.per_job;
+  const int rank = rh / prm.hq;
+  const int head = rh - rank * prm.hq;
+  const int kvh = head / prm.group;
+  const AttnJob job = prm.jobs.far ? prm.jobs.far[ji] : prm.jobs.near[ji];
+  const int m_seen = max(job.first + job.rows - 1, 0);
+  const int n_blk = (m_seen + KA_TILE - 1) / KA_TILE;
+  const bool ragged = (m_seen & (KA_TILE - 1)) != 0;  // the last block reaches past the sequence's keys
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < Cfg::kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(sd_full, 1);
+    mbar_init(sd_free, 8);
+    mbar_init(ds_full, 8);
+    mbar_init(k_raw, 1);
+    mbar_init(scrubbed, 1);
+    mbar_init(dq_done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint64_t tmo = prm.timeout_ns;
+  constexpr uint32_t kDP = KA_TILE, kDQ = 2 * KA_TILE, kDS = 3 * KA_TILE;  // tensor memory columns
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 9) {
+      if (lane == 0 && n_blk > 0) {
+        const uint64_t pol_q = policy_evict_first();
+        const uint64_t pol_kv = policy_evict_last();
+        mbar_arrive_expect_tx(q_full, 2 * Cfg::kTileBytes);
+        for (int b = 0; b < Cfg::kBoxes; ++b) {
+          tma_load_4d(sQ + b * KA_BOX_BYTES, &tmQ, q_full, 64 * b, head, job.q0, rank, pol_q);
+          tma_load_4d(sG + b * KA_BOX_BYTES, &tmG, q_full, 64 * b, head, job.q0, rank, pol_q);
+        }
+        bool ok = true;
+        for (int i = 0; i < 2 * n_blk && ok; ++i) {
+          const int j = i >> 1;
+          const int slot = (i & 1) ? Cfg::v_slot(j) : Cfg::k_slot(j);
+          if (!mbar_wait(&empty[slot], ((j / ((i & 1) ? Cfg::kV : Cfg::kK)) & 1) ^ 1, tmo, 111)) {
+            ok = false;
+            break;
+          }
+          uint64_t* bar = &full[slot];
+          if (ragged && i == 2 * (n_blk - 1)) {
+            bar = k_raw;
+            mbar_arrive(&full[slot]);
+          }
+          mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+          for (int b = 0; b < Cfg::kBoxes; ++b)
+            tma_load_4d(sRing + slot * Cfg::kTileBytes + b * KA_BOX_BYTES, (i & 1) ? &tmV : &tmK, bar, 64 * b, kvh,
+                        job.k0 + j * KA_TILE, rank, pol_kv);
+        }
+        if (!ok) spin_ns(KA_DRAIN_NS);
+      }
+    } else if (warp == 8) {
+      if (lane == 0 && n_blk > 0) {
+        constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KA_TILE);
+        constexpr uint32_t id_q = idesc_bf16_f32_major(KA_TILE, HD, false, true);
+        const uint32_t qa = smem_u32(sQ), ga = smem_u32(sG);
+        auto tile = [&](int slot) { return smem_u32(sRing + slot * Cfg::kTileBytes); };
+        auto scores = [&](int j) {
+          if (!mbar_wait(&full[Cfg::k_slot(j)], (j / Cfg::kK) & 1, tmo, 112)) return false;
+          if (ragged && j == n_blk - 1 && !mbar_wait(scrubbed, 0, tmo, 113)) return false;
+          const uint32_t ka = tile(Cfg::k_slot(j)), va = tile(Cfg::v_slot(j));
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
+            umma_bf16(tmem, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), id_s, kk > 0);
+          }
+          if (!mbar_wait(&full[Cfg::v_slot(j)], (j / Cfg::kV) & 1, tmo, 114)) return false;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
+            umma_bf16(tmem + kDP, sw128_kmajor_desc(ga + off), sw128_kmajor_desc(va + off), id_s, kk > 0);
+          }
+          // also the completion of the product with dS two blocks back, whose buffer comes next
+          umma_commit(sd_full);
+          umma_commit(&empty[Cfg::v_slot(j)]);
+          return true;
+        };
+        bool ok = mbar_wait(q_full, 0, tmo, 115) && scores(0);
+        for (int j = 0; j < n_blk && ok; ++j) {
+          if (j + 1 < n_blk) {
+            ok = mbar_wait(sd_free, j & 1, tmo, 116);
+            if (!ok) break;
+            tc_fence_after();
+            ok = scores(j + 1);
+            if (!ok) break;
+          }
+          ok = mbar_wait(ds_full, j & 1, tmo, 117);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ka = tile(Cfg::k_slot(j));
+#pragma unroll
+          for (int kk = 0; kk < KA_TILE / 16; ++kk)
+            umma_bf16_ts(tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, sw128_mnmajor_desc_128(ka + kk * 2048), id_q,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&empty[Cfg::k_slot(j)]);
+        }
+        umma_commit(dq_done);
+        mbar_wait(dq_done, 0, tmo, 118);
+      }
+    } else if (warp == 10 && ragged) {
+      if (warp_wait(k_raw, 0, tmo, 119)) {
+        uint8_t* k = sRing + Cfg::k_slot(n_blk - 1) * Cfg::kTileBytes;
+        const int live = m_seen - (n_blk - 1) * KA_TILE;
+        for (int b = 0; b < Cfg::kBoxes; ++b)
+          for (int x = live * 8 + lane; x < KA_TILE * 8; x += 32)
+            reinterpret_cast<uint4*>(k + b * KA_BOX_BYTES)[x] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(scrubbed);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int w = warp >> 2;  // which half of the block's keys, and of dQ's columns at the end
+    const int q = warp & 3;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const bool mine = row < job.rows;
+    const int64_t grow = job.q0 + row;
+    const int64_t orow = ((rank * prm.Tq + grow) * prm.hq + head) * prm.dh;
+    const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
+    // D: each thread sums half of its row
+    float part = 0.f;
+    if (mine) {
+#pragma unroll
+      for (int x = 0; x < HD / 16; ++x) {
+        const int e = w * (HD / 2) + 8 * x;
+        if (e < prm.dh) {
+          const uint4 a = ld_nc_v4(prm.out + orow + e), b = ld_nc_v4(prm.dout + orow + e);
+          const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
+            part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
+          }
+        }
+      }
+    }
+    sD[w * KA_TILE + row] = part;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float D = sD[row] + sD[KA_TILE + row];
+    if (mine && w == 0) prm.D[srow] = D;
+    const float c = prm.scale * KA_LOG2E;
+    const float nl = mine ? -prm.lse[srow] * KA_LOG2E : 0.f;
+    const uint64_t c2 = pack_f32x2(c, c), nl2 = pack_f32x2(nl, nl), nd2 = pack_f32x2(-D, -D);
+    const int vis = job.first + row;
+    bool ok = true;
+    for (int j = 0; j < n_blk; ++j) {
+      ok = warp_wait(sd_full, j & 1, tmo, 120);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[64], g[64];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        tmem_ld_32x32b_x32(lanes + 64 * w + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * x));
+        tmem_ld_32x32b_x32(lanes + kDP + 64 * w + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(g + 32 * x));
+      }
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sd_free);
+      const int seen = vis - j * KA_TILE - 64 * w;
+      const bool cut = job.first + q * 32 - j * KA_TILE - 64 * w < 64;
+      uint32_t p[32];
+#pragma unroll
+      for (int y = 0; y < 32; ++y) {
+        float a, b, x0, x1;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, nl2), a, b);
+        unpack_f32x2(mul_f32x2(pack_f32x2(ex2(a), ex2(b)),
+                               add_f32x2(pack_f32x2(__uint_as_float(g[2 * y]), __uint_as_float(g[2 * y + 1])), nd2)),
+                     x0, x1);
+        if (cut) {
+          x0 = 2 * y < seen ? x0 : 0.f;
+          x1 = 2 * y + 1 < seen ? x1 : 0.f;
+        }
+        p[y] = pack_bf16x2(x0, x1);
+      }
+      tmem_st_32x32b_x32(lanes + kDS + (j & 1) * 64 + 32 * w, p);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full);
+    }
+    if (ok && n_blk > 0) ok = warp_wait(dq_done, 0, tmo, 121);
+    tc_fence_after();
+    if (ok) {
+#pragma unroll
+      for (int x = 0; x < HD / 2; x += 32) {
+        const int e = w * (HD / 2) + x;
+        uint32_t o[32];
+        if (n_blk > 0) {
+          tmem_ld_32x32b_x32(lanes + kDQ + e, o);
+          tmem_wait_ld();
+        }
+        if (mine) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (e + 8 * y < prm.dh) {
+              uint32_t v[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float a = __uint_as_float(o[8 * y + 2 * u]) * prm.scale, b = __uint_as_float(o[8 * y + 2 * u + 1]) * prm.scale;
+                v[u] = n_blk > 0 ? pack_bf16x2(a, b) : 0u;
+              }
+              st_v4(prm.dq + orow + e + 8 * y, make_uint4(v[0], v[1], v[2], v[3]));
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+template <int HD>
+struct DkvCfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kTileBytes = kBoxes * KA_BOX_BYTES;         // K or V: 128 keys
+  static constexpr int kQBox = KB2_QT * 128;                       // 64 queries x 64 elements
+  static constexpr int kQBytes = kBoxes * kQBox;                   // Q or dO: 64 queries
+  static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * (2 * kQBytes + 2 * KB2_QT * 4) + 512;
+};
+
+// One CTA: 128 keys of one key head, against its share (1 / splits) of the queries of the group's
+// heads, 64 at a time.  Tensor memory: (S^T | dP^T) of even steps | of odd steps | dV | dK, S^T and
+// dP^T with the keys in the lanes; p^T and dS^T are written over them and are the A operands of the
+// two sums.  Warps 0-3 take the even steps, 4-7 the odd ones: while one set computes, the tensor
+// cores run the other step's products.  Warp 10 passes on every tile of Q and dO: it zeroes the rows
+// behind the sequence's last query and puts lse and D beside the tile.
+//
+// Job: `rows` queries from row q0 on see keys of the tile that starts at row k0 and has k_rows keys:
+// query x sees key y when x >= y + first.
+template <int HD>
+__global__ void __launch_bounds__(KB2_THREADS, 1)
+    attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ BwdAttnParams prm) {
+  using Cfg = DkvCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + Cfg::kTileBytes;
+  uint8_t* sQ = smem + 2 * Cfg::kTileBytes;
+  uint8_t* sG = sQ + Cfg::kStages * Cfg::kQBytes;
+  float* sL = reinterpret_cast<float*>(sG + Cfg::kStages * Cfg::kQBytes);  // [stages][2][64]: -lse log2(e), -D
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sL + Cfg::kStages * 2 * KB2_QT);
+  uint64_t* kv_full = bars;
+  uint64_t* raw = kv_full + 1;             // [stages] TMA
+  uint64_t* full = raw + Cfg::kStages;     // [stages] passed on by warp 10
+  uint64_t* empty = full + Cfg::kStages;   // [stages]
+  uint64_t* sd_full = empty + Cfg::kStages;  // [2]
+  uint64_t* pd_full = sd_full + 2;         // [2] 4 warps
+  uint64_t* done = pd_full + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int ji = blockIdx.x / prm.per_job;
+  int rest = blockIdx.x - ji * prm.per_job;
+  const int split = rest % prm.splits;
+  rest /= prm.splits;
+  const int rank = rest / prm.hk;
+  const int kvh = rest - rank * prm.hk;
+  const AttnJob job = prm.jobs.far ? prm.jobs.far[ji] : prm.jobs.near[ji];
+  const int nt = (job.rows + KB2_QT - 1) / KB2_QT;
+  const int total = nt * prm.group;
+  const int it0 = static_cast<int>(int64_t(total) * split / prm.splits);
+  const int n = static_cast<int>(int64_t(total) * (split + 1) / prm.splits) - it0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < Cfg::kStages; ++s) {
+      mbar_init(&raw[s], 1);
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sd_full[b], 1);
+      mbar_init(&pd_full[b], 4);
+    }
+    mbar_init(done, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmG);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint64_t tmo = prm.timeout_ns;
+  constexpr uint32_t kDV = 4 * KB2_QT, kDK = 4 * KB2_QT + HD;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 9) {
+      if (lane == 0 && n > 0) {
+        const uint64_t pol_kv = policy_evict_first();
+        const uint64_t pol_q = policy_evict_last();
+        mbar_arrive_expect_tx(kv_full, 2 * Cfg::kTileBytes);
+        for (int b = 0; b < Cfg::kBoxes; ++b) {
+          tma_load_4d(sK + b * KA_BOX_BYTES, &tmK, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
+          tma_load_4d(sV + b * KA_BOX_BYTES, &tmV, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
+        }
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+          const int st = i % Cfg::kStages;
+          if (!mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, tmo, 131)) {
+            ok = false;
+            break;
+          }
+          const int h = (it0 + i) / nt, x = (it0 + i) - h * nt;
+          mbar_arrive_expect_tx(&raw[st], 2 * Cfg::kQBytes);
+          for (int b = 0; b < Cfg::kBoxes; ++b) {
+            tma_load_4d(sQ + st * Cfg::kQBytes + b * Cfg::kQBox, &tmQ, &raw[st], 64 * b, kvh * prm.group + h,
+                        job.q0 + x * KB2_QT, rank, pol_q);
+            tma_load_4d(sG + st * Cfg::kQBytes + b * Cfg::kQBox, &tmG, &raw[st], 64 * b, kvh * prm.group + h,
+                        job.q0 + x * KB2_QT, rank, pol_q);
+          }
+        }
+        if (!ok) spin_ns(KA_DRAIN_NS);
+      }
+    } else if (warp == 8) {
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KB2_QT);
+        constexpr uint32_t id_g = idesc_bf16_f32_major(KA_TILE, HD, false, true);
+        const uint32_t ka = smem_u32(sK), va = smem_u32(sV);
+        auto scores = [&](int i) {
+          const int st = i % Cfg::kStages;
+          if (!mbar_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 132)) return false;
+          const uint32_t qa = smem_u32(sQ + st * Cfg::kQBytes), ga = smem_u32(sG + st * Cfg::kQBytes);
+          const uint32_t d = tmem + (i & 1) * 2 * KB2_QT;
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_bf16(d, sw128_kmajor_desc(ka + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
+                      sw128_kmajor_desc(qa + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_bf16(d + KB2_QT, sw128_kmajor_desc(va + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
+                      sw128_kmajor_desc(ga + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
+          umma_commit(&sd_full[i & 1]);
+          return true;
+        };
+        bool ok = mbar_wait(kv_full, 0, tmo, 133) && scores(0) && (n < 2 || scores(1));
+        for (int i = 0; i < n && ok; ++i) {
+          ok = mbar_wait(&pd_full[i & 1], (i >> 1) & 1, tmo, 134);
+          if (!ok) break;
+          tc_fence_after();
+          const int st = i % Cfg::kStages;
+          const uint32_t qa = smem_u32(sQ + st * Cfg::kQBytes), ga = smem_u32(sG + st * Cfg::kQBytes);
+          const uint32_t a = tmem + (i & 1) * 2 * KB2_QT;
+#pragma unroll
+          for (int kk = 0; kk < KB2_QT / 16; ++kk)
+            umma_bf16_ts(tmem + kDV, a + 8 * kk, sw128_mnmajor_desc(ga + kk * 2048), id_g, (i > 0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < KB2_QT / 16; ++kk)
+            umma_bf16_ts(tmem + kDK, a + KB2_QT + 8 * kk, sw128_mnmajor_desc(qa + kk * 2048), id_g,
+                         (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&empty[st]);
+          if (i + 2 < n) ok = scores(i + 2);
+        }
+        umma_commit(done);
+        mbar_wait(done, 0, tmo, 135);
+      }
+    } else if (warp == 10) {
+      for (int i = 0; i < n; ++i) {
+        const int st = i % Cfg::kStages;
+        const uint32_t ph = (i / Cfg::kStages) & 1;
+        const int h = (it0 + i) / nt, x = ((it0 + i) - h * nt) * KB2_QT;
+        const int live = min(job.rows - x, KB2_QT);
+        const int64_t srow = (int64_t(rank) * prm.hq + kvh * prm.group + h) * prm.Tq + job.q0 + x;
+        float v[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int y = lane + 32 * u;
+          v[u] = y < live ? -prm.lse[srow + y] * KA_LOG2E : 0.f;
+          v[2 + u] = y < live ? -prm.D[srow + y] : 0.f;
+        }
+        if (!warp_wait(&raw[st], ph, tmo, 136)) break;
+        float* l = sL + st * 2 * KB2_QT;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          l[lane + 32 * u] = v[u];
+          l[KB2_QT + lane + 32 * u] = v[2 + u];
+        }
+        if (live < KB2_QT) {
+          for (int b = 0; b < Cfg::kBoxes; ++b)
+            for (int y = live * 8 + lane; y < KB2_QT * 8; y += 32) {
+              reinterpret_cast<uint4*>(sQ + st * Cfg::kQBytes + b * Cfg::kQBox)[y] = make_uint4(0, 0, 0, 0);
+              reinterpret_cast<uint4*>(sG + st * Cfg::kQBytes + b * Cfg::kQBox)[y] = make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int w = warp >> 2;
+    const int q = warp & 3;
+    const int row = q * 32 + lane;  // key
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const float c = prm.scale * KA_LOG2E;
+    const uint64_t c2 = pack_f32x2(c, c);
+    bool ok = true;
+    for (int i = w; i < n; i += 2) {
+      const int st = i % Cfg::kStages;
+      ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 137) && warp_wait(&sd_full[w], (i >> 1) & 1, tmo, 138);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t base = lanes + w * 2 * KB2_QT;
+      uint32_t s[64], g[64];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        tmem_ld_32x32b_x32(base + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * x));
+        tmem_ld_32x32b_x32(base + KB2_QT + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(g + 32 * x));
+      }
+      tmem_wait_ld();
+      const int h = (it0 + i) / nt, x0 = ((it0 + i) - h * nt) * KB2_QT;
+      const int lo = row + job.first - x0;    // the key is seen from this query of the step on
+      const int hi = job.rows - x0;           // queries of the step
+      const bool cut = hi < KB2_QT || q * 32 + 31 + job.first > x0;
+      const float4* l = reinterpret_cast<const float4*>(sL + st * 2 * KB2_QT);
+      uint32_t pp[32], pd[32];
+#pragma unroll
+      for (int y = 0; y < 16; ++y) {  // four queries at a time
+        const float4 nl = l[y], nd = l[16 + y];
+        float a[4], d[4];
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[4 * y]), __uint_as_float(s[4 * y + 1])), c2, pack_f32x2(nl.x, nl.y)), a[0], a[1]);
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[4 * y + 2]), __uint_as_float(s[4 * y + 3])), c2, pack_f32x2(nl.z, nl.w)), a[2], a[3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) a[u] = ex2(a[u]);
+        unpack_f32x2(mul_f32x2(pack_f32x2(a[0], a[1]), add_f32x2(pack_f32x2(__uint_as_float(g[4 * y]), __uint_as_float(g[4 * y + 1])), pack_f32x2(nd.x, nd.y))), d[0], d[1]);
+        unpack_f32x2(mul_f32x2(pack_f32x2(a[2], a[3]), add_f32x2(pack_f32x2(__uint_as_float(g[4 * y + 2]), __uint_as_float(g[4 * y + 3])), pack_f32x2(nd.z, nd.w))), d[2], d[3]);
+        if (cut) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool see = 4 * y + u >= lo && 4 * y + u < hi;
+            a[u] = see ? a[u] : 0.f;
+            d[u] = see ? d[u] : 0.f;
+          }
+        }
+        pp[2 * y] = pack_bf16x2(a[0], a[1]);
+        pp[2 * y + 1] = pack_bf16x2(a[2], a[3]);
+        pd[2 * y] = pack_bf16x2(d[0], d[1]);
+        pd[2 * y + 1] = pack_bf16x2(d[2], d[3]);
+      }
+      tmem_st_32x32b_x32(base, pp);
+      tmem_st_32x32b_x32(base + KB2_QT, pd);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pd_full[w]);
+    }
+    if (ok && n > 0) ok = warp_wait(done, 0, tmo, 139);
+    tc_fence_after();
+    if (ok) {
+      // warps 0-3 store dV, 4-7 dK
+      const bool mine = row < job.k_rows;
+      const float f = w ? prm.scale : 1.f;
+      const int64_t krow = ((rank * prm.Tk + job.k0 + row) * prm.hk + kvh) * prm.dh;
+      const int64_t all = prm.P * prm.Tk * prm.hk * prm.dh;
+      __nv_bfloat16* dst = (w ? prm.dk : prm.dv) + krow;
+      float* pdst = prm.part + (w * prm.splits + split) * all + krow;
+#pragma unroll
+      for (int x = 0; x < HD; x += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld_32x32b_x32(lanes + (w ? kDK : kDV) + x, o);
+          tmem_wait_ld();
+        }
+        if (mine) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (x + 8 * y < prm.dh) {
+              float v[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) v[u] = n > 0 ? __uint_as_float(o[8 * y + u]) * f : 0.f;
+              if (prm.splits > 1) {
+                *reinterpret_cast<float4*>(pdst + x + 8 * y) = make_float4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<float4*>(pdst + x + 8 * y + 4) = make_float4(v[4], v[5], v[6], v[7]);
+              } else {
+                st_v4(dst + x + 8 * y, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                                  pack_bf16x2(v[6], v[7])));
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// dk, dv of a job's keys from the partial sums, added in the order of the splits.
+__global__ void __launch_bounds__(256) attn_dkv_join_kernel(const __grid_constant__ BwdAttnParams prm) {
+  const AttnJob job = prm.jobs.far ? prm.jobs.far[blockIdx.x] : prm.jobs.near[blockIdx.x];
+  const int rank = blockIdx.y;
+  const int vecs = prm.hk * prm.dh / 4;  // a key's row over all heads
+  const int64_t all = prm.P * prm.Tk * prm.hk * prm.dh;
+  const int64_t base = (rank * prm.Tk + job.k0) * prm.hk * prm.dh;
+  for (int i = threadIdx.x + blockIdx.z * 256; i < job.k_rows * vecs; i += 256 * gridDim.z) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int z = 0; z < prm.splits; ++z) {
+        const float4 v = *reinterpret_cast<const float4*>(prm.part + (w * prm.splits + z) * all + base + 4 * i);
+        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+      }
+      *reinterpret_cast<uint2*>((w ? prm.dk : prm.dv) + base + 4 * i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+}
+
+}  // namespace caat

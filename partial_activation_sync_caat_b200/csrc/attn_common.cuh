@@ -17,6 +17,7 @@ constexpr float KA_LN2 = 0.6931471805599453f;
 // min(first + i, m) of them, and never fewer than 0.
 struct AttnJob {
   int q0, rows, k0, first;
+  int k_rows;  // dkv only
 };
 
 // Work lists travel in the launch's arguments when they fit, else through the workspace.

@@ -14,15 +14,6 @@ struct AttnView {            // a strided [P, T, heads, dh] operand
   int64_t rank, tok;
 };
 
-struct AttnSimple {
-  AttnView q, k, v;
-  __nv_bfloat16* out;
-  float* lse;
-  int64_t Tq, Tk;
-  int hq, hk, dh;
-  float scale;
-};
-
 __device__ __forceinline__ float4 ld_row4(const __nv_bfloat16* p, int e, int dh) {
   if (e >= dh) return make_float4(0.f, 0.f, 0.f, 0.f);
   const uint2 w = *reinterpret_cast<const uint2*>(p + e);
@@ -45,57 +36,6 @@ __device__ __forceinline__ void axpy4(float4& o, float a, float4 x) {
   o.y = fmaf(a, x.y, o.y);
   o.z = fmaf(a, x.z, o.z);
   o.w = fmaf(a, x.w, o.w);
-}
-
-struct AttnSimpleBwd {
-  AttnSimple f;
-  const __nv_bfloat16* dout;
-  __nv_bfloat16 *dq, *dk, *dv;
-  float* D;                  // [P, hq, Tq]
-};
-
-__global__ void __launch_bounds__(128) attn_simple_dq_kernel(AttnSimpleBwd b, int q0, int n, int k0, int m) {
-  const AttnSimple& a = b.f;
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, e = 4 * lane;
-  if (i >= n) return;
-  const int h = blockIdx.y, r = blockIdx.z, kv = h / (a.hq / a.hk);
-  const int64_t row = q0 + i, orow = ((r * a.Tq + row) * a.hq + h) * a.dh, srow = (int64_t(r) * a.hq + h) * a.Tq + row;
-  const float4 q = ld_row4(a.q.p + r * a.q.rank + row * a.q.tok + h * a.dh, e, a.dh);
-  const float4 g = ld_row4(b.dout + orow, e, a.dh);
-  const float D = warp_dot4(g, ld_row4(a.out + orow, e, a.dh)), lse = a.lse[srow];
-  if (lane == 0) b.D[srow] = D;
-  float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int seen = i + 1 + (m - n);
-  for (int j = 0; j < seen; ++j) {
-    const float4 k = ld_row4(a.k.p + r * a.k.rank + int64_t(k0 + j) * a.k.tok + kv * a.dh, e, a.dh);
-    const float4 v = ld_row4(a.v.p + r * a.v.rank + int64_t(k0 + j) * a.v.tok + kv * a.dh, e, a.dh);
-    const float p = expf(a.scale * warp_dot4(q, k) - lse);
-    axpy4(dq, a.scale * p * (warp_dot4(g, v) - D), k);
-  }
-  st_row4(b.dq + orow, e, a.dh, dq);
-}
-
-__global__ void __launch_bounds__(128) attn_simple_dkv_kernel(AttnSimpleBwd b, int q0, int n, int k0, int m) {
-  const AttnSimple& a = b.f;
-  const int j = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, e = 4 * lane;
-  if (j >= m) return;
-  const int kv = blockIdx.y, r = blockIdx.z, group = a.hq / a.hk;
-  const float4 k = ld_row4(a.k.p + r * a.k.rank + int64_t(k0 + j) * a.k.tok + kv * a.dh, e, a.dh);
-  const float4 v = ld_row4(a.v.p + r * a.v.rank + int64_t(k0 + j) * a.v.tok + kv * a.dh, e, a.dh);
-  float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-  for (int h = kv * group; h < (kv + 1) * group; ++h) {
-    for (int i = max(0, j - (m - n)); i < n; ++i) {
-      const int64_t row = q0 + i, srow = (int64_t(r) * a.hq + h) * a.Tq + row;
-      const float4 q = ld_row4(a.q.p + r * a.q.rank + row * a.q.tok + h * a.dh, e, a.dh);
-      const float4 g = ld_row4(b.dout + ((r * a.Tq + row) * a.hq + h) * a.dh, e, a.dh);
-      const float p = expf(a.scale * warp_dot4(q, k) - a.lse[srow]);
-      axpy4(dv, p, g);
-      axpy4(dk, a.scale * p * (warp_dot4(g, v) - b.D[srow]), q);
-    }
-  }
-  const int64_t krow = ((r * a.Tk + k0 + j) * a.hk + kv) * a.dh;
-  st_row4(b.dk + krow, e, a.dh, dk);
-  st_row4(b.dv + krow, e, a.dh, dv);
 }
 
 // Decoding: one warp per (rank, sequence, head).
