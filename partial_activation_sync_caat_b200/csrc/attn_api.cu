@@ -15,8 +15,8 @@
 #include "host_common.h"
 #include "ptx.cuh"
 #include "attn_bwd.cuh"
+#include "attn_decode.cuh"
 #include "attn_fwd.cuh"
-#include "attn_simple.cuh"
 #include "rope.cuh"
 
 namespace caat {
@@ -82,8 +82,6 @@ Range range_of(const void* p, size_t bytes) {
 bool meet(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 Range range_of(const View& v) { return {v.lo, v.hi}; }
 
-caat::AttnView device_view(const View& v) { return {reinterpret_cast<const __nv_bfloat16*>(v.p), v.rank, v.tok}; }
-
 caat_status check_heads(int P, int hq, int hk, int dh, float scale) {
   if (P < 1 || P > CAAT_MAX_P || hq < 1 || hk < 1 || dh < 1) return CAAT_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return CAAT_ERR_INVALID_ARG;
@@ -115,6 +113,7 @@ caat_status attn_setup(int* sms) {
   };
   if (!smem(caat::attn_fwd_kernel<64>, caat::FwdCfg<64>::kSmem) || !smem(caat::attn_fwd_kernel<128>, caat::FwdCfg<128>::kSmem) ||
       !smem(caat::attn_dq_kernel<64>, caat::DqCfg<64>::kSmem) || !smem(caat::attn_dq_kernel<128>, caat::DqCfg<128>::kSmem) ||
+      !smem(caat::attn_decode_kernel<64>, caat::KD_SMEM) || !smem(caat::attn_decode_kernel<128>, caat::KD_SMEM) ||
       !smem(caat::attn_dkv_kernel<64>, caat::DkvCfg<64>::kSmem) || !smem(caat::attn_dkv_kernel<128>, caat::DkvCfg<128>::kSmem))
     return CAAT_ERR_CUDA;
   done[dev] = ctx;
@@ -448,7 +447,8 @@ size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int he
   switch (variant) {
     case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
     case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : bwd_layout(Tq, Tk, n_seq, P, heads_q, heads_k, dh).total;
-    case CAAT_VARIANT_ATTN_DECODE: return 0;
+    case CAAT_VARIANT_ATTN_DECODE:
+      return align256(size_t(caat::KD_CTAS) * 2 * std::min(heads_q / heads_k, 16) * (dh + 2) * 4);
   }
   return SIZE_MAX;
 }
@@ -545,7 +545,7 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   caat_status s = check_heads(a->P, a->heads_q, a->heads_k, a->dh, a->scale);
   if (s != CAAT_OK) return s;
   if (a->B < 0 || a->capacity < 0 || a->flags != 0) return CAAT_ERR_INVALID_ARG;
-  if (a->capacity > kMaxRows || a->B > 65535) return CAAT_ERR_UNSUPPORTED;
+  if (a->capacity > kMaxRows || a->B > caat::KD_MAX_B) return CAAT_ERR_UNSUPPORTED;
   if (a->B == 0) return CAAT_OK;
   View q;
   if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->B, a->heads_q, a->dh)) != CAAT_OK) return s;
@@ -557,17 +557,60 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   if (meet(out, range_of(q)) || meet(out, range_of(a->k_cache, cache)) || meet(out, range_of(a->v_cache, cache)) ||
       meet(out, range_of(a->lens, size_t(a->B) * 4)))
     return CAAT_ERR_INVALID_ARG;
+  const size_t need = caat_attn_workspace_size(a->B, a->capacity, 0, a->P, a->heads_q, a->heads_k, a->dh, CAAT_VARIANT_ATTN_DECODE);
+  if (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) return CAAT_ERR_WORKSPACE;
   int sms = 0;
-  if ((s = caat::host::device_sms(&sms)) != CAAT_OK) return s;
-  caat::AttnSimpleDecode p{device_view(q), reinterpret_cast<const __nv_bfloat16*>(a->k_cache),
-                           reinterpret_cast<const __nv_bfloat16*>(a->v_cache), a->lens,
-                           reinterpret_cast<__nv_bfloat16*>(a->out), a->B, a->capacity, a->heads_q, a->heads_k, a->dh,
-                           a->scale};
+  if ((s = attn_setup(&sms)) != CAAT_OK) return s;
+  caat::DecodeAttnParams p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(a->q);
+  p.k = reinterpret_cast<const __nv_bfloat16*>(a->k_cache);
+  p.v = reinterpret_cast<const __nv_bfloat16*>(a->v_cache);
+  p.lens = a->lens;
+  p.out = reinterpret_cast<__nv_bfloat16*>(a->out);
+  p.part = static_cast<float*>(a->workspace);
+  p.q_rank = q.rank;
+  p.q_tok = q.tok;
+  p.B = a->B;
+  p.capacity = a->capacity;
+  p.P = a->P;
+  p.hq = a->heads_q;
+  p.hk = a->heads_k;
+  p.dh = a->dh;
+  p.group = a->heads_q / a->heads_k;
+  p.rows = std::min(p.group, 16);
+  p.n_gb = (p.group + 15) / 16;
+  p.G = a->P * a->heads_k * p.n_gb;
+  p.scale = a->scale;
+  const int HD = a->dh <= 64 ? 64 : 128;
+  const int stage = 4 * 2 * 16 * HD * 2, index = static_cast<int>(a->B + 5) * 4;
+  const int merge = 4 * p.rows * (HD + 2) * 4;
+  p.stages = std::min(5, (caat::KD_SMEM - merge - index) / stage);
+  const int bytes = p.stages * stage + merge + index;
+  const int64_t most = int64_t(p.G) * a->B * ((a->capacity + caat::KD_TILE - 1) / caat::KD_TILE);
+  const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(caat::KD_CTAS, most)));
   Recorder rec;
   rec.begin(a->timing, a->stream);
-  caat::attn_simple_decode_kernel<<<dim3(static_cast<unsigned>(a->B), a->heads_q, a->P), 32, 0, a->stream>>>(p);
+  if (HD == 64)
+    caat::attn_decode_kernel<64><<<ctas, caat::KD_THREADS, bytes, a->stream>>>(p);
+  else
+    caat::attn_decode_kernel<128><<<ctas, caat::KD_THREADS, bytes, a->stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
+  if (ctas > 1) {
+    // launched while the first kernel still runs; it waits for it before reading the partial results
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(ctas - 1, 1, 1);
+    cfg.blockDim = dim3(caat::KD_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = index;
+    cfg.stream = a->stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, caat::attn_decode_join_kernel, p, ctas) != cudaSuccess) return CAAT_ERR_CUDA;
+    rec.after_kernel(a->stream);
+  }
   return CAAT_OK;
 }
 

@@ -1,0 +1,395 @@
+// attn_decode.cuh - one new token per sequence against its cache, on every rank.
+//
+// Every byte of K and V is used once, so the read rate of the memory bounds it.  The work is the list of
+// 64-key tiles of all (sequence, rank, key head) segments; it is cut evenly over a fixed number of
+// CTAs, whatever the lengths, so that one long sequence and many short ones alike keep all SMs
+// reading.  A segment cut between CTAs leaves fp32 partial results (maximum, sum, sums of p v) that a
+// second kernel joins, in the order of the CTAs.
+//
+// Inside a CTA each of the 4 warps owns 16 of a tile's keys and a ring of its own, filled with
+// 16-byte asynchronous copies: no block-wide waits until a segment ends, when the warps' running
+// maxima, sums and products are merged through shared memory.  Up to 16 query heads of the group share
+// the tile as the 16 rows of the MMA (legacy mma.sync: the products are a small part of the time even
+// with one head of the 16 rows in use: 64 keys x 128 elements of K and V are 32 KiB, about 1400 clocks of
+// an SM's share of the memory rate, against 128 MMAs).  Keys past the length are never read: their rows
+// are filled with zeros, their scores replaced by -inf.
+#pragma once
+
+#include "attn_common.cuh"
+#include "rope.cuh"
+
+namespace caat {
+
+constexpr int KD_THREADS = 128;
+constexpr int KD_TILE = 64;        // keys of a tile: 16 per warp
+constexpr int KD_CTAS = 296;       // two per SM
+constexpr int KD_MAX_B = 4096;
+constexpr int KD_SMEM = 113 * 1024;
+
+struct DecodeAttnParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;      // [P, B, capacity, hk, dh]
+  const __nv_bfloat16* v;
+  const int32_t* lens;
+  __nv_bfloat16* out;          // [P, B, hq, dh]
+  float* part;                 // [CTAs][2][rows][dh + 2]: sums of p v, maximum (scaled, base 2), sum of p
+  int64_t q_rank, q_tok;
+  int64_t B, capacity;
+  int P, hq, hk, dh, group;
+  int rows;                    // min(group, 16)
+  int n_gb;                    // blocks of 16 heads in a group
+  int G;                       // segments of a sequence: P * hk * n_gb
+  int stages;
+  float scale;
+};
+
+// pre[b] = tiles of the sequences before b, pre[B] = all of them.  A length outside the cache counts as 0.
+__device__ __forceinline__ void decode_prefix(const DecodeAttnParams& prm, int* pre, int* warp_sums) {
+  const int B = static_cast<int>(prm.B);
+  const int per = (B + KD_THREADS - 1) / KD_THREADS;
+  const int b0 = threadIdx.x * per;
+  int sum = 0;
+  for (int b = b0; b < min(b0 + per, B); ++b) {
+    const int len = __ldg(prm.lens + b);
+    sum += (len > 0 && len <= prm.capacity) ? (len + KD_TILE - 1) / KD_TILE : 0;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int at = inc - sum;
+  for (int w = 0; w < warp; ++w) at += warp_sums[w];
+  for (int b = b0; b < min(b0 + per, B); ++b) {
+    pre[b] = at;
+    const int len = __ldg(prm.lens + b);
+    at += (len > 0 && len <= prm.capacity) ? (len + KD_TILE - 1) / KD_TILE : 0;
+  }
+  if (b0 < B && b0 + per >= B) pre[B] = at;
+  __syncthreads();
+}
+
+// A tile of the work list: sequence, segment of the sequence, tile of the segment.
+struct DecodeCursor {
+  int b, g, t, tiles;
+  __device__ __forceinline__ void seek(const DecodeAttnParams& prm, const int* pre, int64_t item) {
+    int lo = 0, hi = static_cast<int>(prm.B);  // pre[lo] G <= item < pre[hi] G
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (int64_t(pre[mid]) * prm.G <= item) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    tiles = pre[b + 1] - pre[b];
+    const int64_t in = item - int64_t(pre[b]) * prm.G;
+    g = static_cast<int>(in / tiles);
+    t = static_cast<int>(in - int64_t(g) * tiles);
+  }
+  __device__ __forceinline__ void next(const DecodeAttnParams& prm, const int* pre) {
+    if (++t < tiles) return;
+    t = 0;
+    if (++g < prm.G) return;
+    g = 0;
+    do {
+      ++b;
+    } while (b < prm.B && pre[b + 1] == pre[b]);
+    if (b < prm.B) tiles = pre[b + 1] - pre[b];
+  }
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid_constant__ DecodeAttnParams prm) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int kRow = HD * 2;                 // bytes of a key's row in shared memory
+  constexpr int kStage = 2 * 16 * kRow;        // a warp's 16 keys of K and of V
+  constexpr int kChunks = HD / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem_raw + warp * prm.stages * kStage;
+  float* merge = reinterpret_cast<float*>(smem_raw + 4 * prm.stages * kStage);  // [4][rows][HD]
+  float* ml = merge + 4 * prm.rows * HD;                                        // [4][rows][2]
+  int* pre = reinterpret_cast<int*>(ml + 4 * prm.rows * 2);                     // [B + 1]
+  int* warp_sums = pre + prm.B + 1;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  decode_prefix(prm, pre, warp_sums);
+  // sequences without keys
+  for (int64_t b = blockIdx.x; b < prm.B; b += gridDim.x) {
+    if (pre[b + 1] != pre[b]) continue;
+    if (threadIdx.x == 0 && __ldg(prm.lens + b) != 0) atomicCAS(&g_arg_status, 0, (82 << 8) | 1);
+    const int n = prm.hq * prm.dh / 8;
+    for (int r = 0; r < prm.P; ++r)
+      for (int i = threadIdx.x; i < n; i += KD_THREADS)
+        st_v4(prm.out + (r * prm.B + b) * prm.hq * prm.dh + 8 * i, make_uint4(0, 0, 0, 0));
+  }
+  const int64_t total = int64_t(pre[prm.B]) * prm.G;
+  const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
+  if (i0 == i1) return;
+
+  DecodeCursor ld, at;
+  ld.seek(prm, pre, i0);
+  at = ld;
+  int64_t todo = i1 - i0;
+  // segment g of a sequence: head block fastest, then key head, then rank
+  auto split_g = [&](int g, int& rank, int& kvh, int& gb) {
+    gb = g % prm.n_gb;
+    const int x = g / prm.n_gb;
+    rank = x / prm.hk;
+    kvh = x - rank * prm.hk;
+  };
+  auto load = [&](int stage) {
+    if (todo > 0) {
+      int rank, kvh, gb;
+      split_g(ld.g, rank, kvh, gb);
+      const int key0 = ld.t * KD_TILE + warp * 16;
+      const int live = __ldg(prm.lens + ld.b) - key0;
+      const int64_t tok = int64_t(prm.hk) * prm.dh;
+      const int64_t base = ((rank * prm.B + ld.b) * prm.capacity + key0) * tok + int64_t(kvh) * prm.dh;
+      const uint32_t dst = smem_u32(ring + stage * kStage);
+#pragma unroll
+      for (int i = 0; i < 16 * kChunks / 32; ++i) {
+        const int x = i * 32 + lane;
+        const int r = x / kChunks, ch = x % kChunks;
+        const bool in = r < live && ch * 8 < prm.dh;
+        const int64_t off = in ? base + r * tok + ch * 8 : 0;
+        const uint32_t d = dst + r * kRow + ((ch ^ (r & 7)) << 4);
+        cp_async_16(d, prm.k + off, in ? 16 : 0);
+        cp_async_16(d + 16 * kRow, prm.v + off, in ? 16 : 0);
+      }
+      --todo;
+      ld.next(prm, pre);
+    }
+    cp_async_commit();
+  };
+
+  for (int s = 0; s < prm.stages - 1; ++s) load(s);
+  const float c = prm.scale * KA_LOG2E;
+  const int r0 = lane >> 2;  // the thread's rows: r0, r0 + 8
+  uint32_t qa[HD / 16][4];
+  float o[HD / 8][4];
+  float m[2], l[2];
+  bool fresh = true;
+  int stage = 0, ld_stage = prm.stages - 1;
+  for (int64_t left = i1 - i0; left > 0; --left) {
+    int rank, kvh, gb;
+    split_g(at.g, rank, kvh, gb);
+    const int rows = min(prm.group - 16 * gb, 16);
+    const int head0 = kvh * prm.group + 16 * gb;
+    if (fresh) {
+      const __nv_bfloat16* q = prm.q + rank * prm.q_rank + at.b * prm.q_tok + int64_t(head0) * prm.dh;
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = r0 + 8 * (e & 1), d = 16 * kk + 8 * (e >> 1) + 2 * (lane & 3);
+          qa[kk][e] = (r < rows && d < prm.dh) ? *reinterpret_cast<const uint32_t*>(q + r * prm.dh + d) : 0u;
+        }
+#pragma unroll
+      for (int x = 0; x < HD / 8; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+      fresh = false;
+    }
+    load(ld_stage);
+    ld_stage = ld_stage + 1 == prm.stages ? 0 : ld_stage + 1;
+    switch (prm.stages) {
+      case 2: cp_async_wait<1>(); break;
+      case 3: cp_async_wait<2>(); break;
+      case 4: cp_async_wait<3>(); break;
+      default: cp_async_wait<4>(); break;
+    }
+    __syncwarp();
+    const uint32_t ks = smem_u32(ring + stage * kStage), vs = ks + 16 * kRow;
+    const int live = __ldg(prm.lens + at.b) - (at.t * KD_TILE + warp * 16);
+    if (live > 0) {
+      float s[2][4] = {};
+      const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;  // ldmatrix row and chunk of the lane
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        uint32_t b[4];
+        ldmatrix_x4(ks + kr * kRow + (((2 * kk + kc) ^ (kr & 7)) << 4), b);
+        mma_16816(s[0], qa[kk], b[0], b[1]);
+        mma_16816(s[1], qa[kk], b[2], b[3]);
+      }
+      float top[2] = {m[0], m[1]};
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 8 * x + 2 * (lane & 3) + (e & 1);
+          s[x][e] = key < live ? s[x][e] * c : -INFINITY;
+          top[e >> 1] = fmaxf(top[e >> 1], s[x][e]);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
+        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
+      }
+      if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float f = top[e] > m[e] ? ex2(m[e] - top[e]) : 1.f;
+          m[e] = top[e];
+          l[e] *= f;
+#pragma unroll
+          for (int x = 0; x < HD / 8; ++x) {
+            o[x][2 * e] *= f;
+            o[x][2 * e + 1] *= f;
+          }
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base = m[e] == -INFINITY ? 0.f : m[e];
+          const float p0 = ex2(s[x][2 * e] - base), p1 = ex2(s[x][2 * e + 1] - base);
+          l[e] += p0 + p1;
+          pa[2 * x + e] = pack_bf16x2(p0, p1);
+        }
+      const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+#pragma unroll
+      for (int x = 0; x < HD / 16; ++x) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(vs + vr * kRow + (((2 * x + vc) ^ (vr & 7)) << 4), b);
+        mma_16816(o[2 * x], pa, b[0], b[1]);
+        mma_16816(o[2 * x + 1], pa, b[2], b[3]);
+      }
+    }
+    __syncwarp();
+    stage = stage + 1 == prm.stages ? 0 : stage + 1;
+
+    const bool ends = at.t + 1 == at.tiles;
+    if (ends || left == 1) {
+      // the CTA's part of the segment: merge the four warps
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+        const int r = r0 + 8 * e;
+        if (r < rows) {
+          float* row = merge + (warp * prm.rows + r) * HD;
+#pragma unroll
+          for (int x = 0; x < HD / 8; ++x)
+            *reinterpret_cast<float2*>(row + 8 * x + 2 * (lane & 3)) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
+          if ((lane & 3) == 0) {
+            ml[(warp * prm.rows + r) * 2] = m[e];
+            ml[(warp * prm.rows + r) * 2 + 1] = l[e];
+          }
+        }
+      }
+      __syncthreads();
+      const bool starts_here = left + at.t <= i1 - i0;  // the segment's first tile is this CTA's
+      const bool complete = ends && starts_here;
+      float* part = prm.part + (int64_t(blockIdx.x) * 2 + (starts_here ? 1 : 0)) * prm.rows * (prm.dh + 2);
+      for (int i = threadIdx.x; i < rows * (prm.dh / 2); i += KD_THREADS) {
+        const int r = i / (prm.dh / 2), d = 2 * (i - r * (prm.dh / 2));
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[(w * prm.rows + r) * 2]);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = ex2(ml[(w * prm.rows + r) * 2] - base);
+          const float2 x = *reinterpret_cast<const float2*>(merge + (w * prm.rows + r) * HD + d);
+          L = fmaf(f, ml[(w * prm.rows + r) * 2 + 1], L);
+          x0 = fmaf(f, x.x, x0);
+          x1 = fmaf(f, x.y, x1);
+        }
+        if (complete) {
+          const float inv = 1.f / L;
+          *reinterpret_cast<uint32_t*>(prm.out + ((rank * prm.B + at.b) * prm.hq + head0 + r) * prm.dh + d) =
+              pack_bf16x2(x0 * inv, x1 * inv);
+        } else {
+          float* p = part + r * (prm.dh + 2);
+          p[d] = x0;
+          p[d + 1] = x1;
+          if (d == 0) {
+            p[prm.dh] = M;
+            p[prm.dh + 1] = L;
+          }
+        }
+      }
+      __syncthreads();
+      fresh = true;
+    }
+    at.next(prm, pre);
+  }
+}
+
+// Joins the segments that a boundary between CTAs cuts: block c - 1 takes the segment that boundary c is
+// the first to cut.
+__global__ void __launch_bounds__(KD_THREADS) attn_decode_join_kernel(const __grid_constant__ DecodeAttnParams prm, int ctas) {
+  extern __shared__ int pre[];
+  int* warp_sums = pre + prm.B + 1;
+  decode_prefix(prm, pre, warp_sums);
+  // every block waits for the partial results, so that this kernel never ends before the first one
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x + 1;
+  const int64_t total = int64_t(pre[prm.B]) * prm.G;
+  const int64_t cut = total * c / ctas, before = total * (c - 1) / ctas;
+  if (cut == before || cut >= total) return;  // CTA c - 1 had nothing, or nothing follows
+  DecodeCursor at;
+  at.seek(prm, pre, cut);
+  const int64_t begin = cut - at.t, end = begin + at.tiles;
+  if (at.t == 0 || begin < before) return;
+  int last = c;  // the last CTA with tiles of the segment
+  while (total * (last + 1) / ctas < end) ++last;
+  const int gb = at.g % prm.n_gb, x = at.g / prm.n_gb, rank = x / prm.hk, kvh = x - rank * prm.hk;
+  const int rows = min(prm.group - 16 * gb, 16);
+  const int64_t stride = int64_t(prm.rows) * (prm.dh + 2);
+  // with fewer tiles than CTAs some CTAs have none and left nothing
+  auto had_tiles = [&](int z) { return total * (z + 1) / ctas > total * z / ctas; };
+  for (int i = threadIdx.x; i < rows * (prm.dh / 2); i += KD_THREADS) {
+    const int r = i / (prm.dh / 2), d = 2 * (i - r * (prm.dh / 2));
+    const float* p0 = prm.part + r * (prm.dh + 2);
+    // the CTA that begins the segment left it in its slot 1, the others in their slot 0
+    float M = -INFINITY;
+    for (int z = c - 1; z <= last; ++z)
+      if (had_tiles(z)) M = fmaxf(M, p0[(2 * int64_t(z) + (z == c - 1)) * stride + prm.dh]);
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, x0 = 0.f, x1 = 0.f;
+    for (int z = c - 1; z <= last; ++z) {
+      if (!had_tiles(z)) continue;
+      const float* p = p0 + (2 * int64_t(z) + (z == c - 1)) * stride;
+      const float f = ex2(p[prm.dh] - base);
+      L = fmaf(f, p[prm.dh + 1], L);
+      x0 = fmaf(f, p[d], x0);
+      x1 = fmaf(f, p[d + 1], x1);
+    }
+    const float inv = 1.f / L;
+    *reinterpret_cast<uint32_t*>(prm.out + ((rank * prm.B + at.b) * prm.hq + kvh * prm.group + 16 * gb + r) * prm.dh + d) =
+        pack_bf16x2(x0 * inv, x1 * inv);
+  }
+}
+
+}  // namespace caat

@@ -168,6 +168,8 @@ def test_decode_refuses(L):
     for kw in (dict(dh=132), dict(dh=136), dict(k_cache=0x10000008), dict(lens=0x3000002), dict(B=65536),
                dict(capacity=(1 << 30) + 1)):
         assert decode(L, **kw) == C.CAAT_ERR_UNSUPPORTED, kw
+    for kw in (dict(workspace=None), dict(ws_bytes=1024), dict(workspace=0x6000010)):
+        assert decode(L, **kw) == C.CAAT_ERR_WORKSPACE, kw
     assert decode(L, B=0, q=None) == C.CAAT_OK
 
 
