@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -175,6 +176,7 @@ class AttnDecodeArgs(ctypes.Structure):
     ]
 
 
+_SIZE_MAX = ctypes.c_size_t(-1).value
 _lib = None
 
 
@@ -608,78 +610,112 @@ def caat_rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none
     return f, float(m.value)
 
 
-def _on_current_device(dev):
-    """The library queues on the current device: tensors of another one are refused."""
+def _current(t, name):
+    """Index of the tensor's device, which has to be the current one: the library queues there."""
     import torch
-    if dev.type != "cuda":
-        raise ValueError("tensors must be CUDA tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _like(t, name, dtype, shape, device, contiguous=True):
+def _raw_stream(stream, dev):
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _like(t, name, dtype, shape, dev, contiguous=True):
     """Address of a tensor after checks of its type, shape, device and layout."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _heads4(t, name, dtype, device, shape=None):
+def _heads4(t, name, dtype, dev, shape=None):
     """Address and (rank, token) strides of a [P, T, heads, dh] tensor whose heads lie side by side
     within a token (a contiguous tensor, or a slice of a fused projection)."""
     if t.dim() != 4:
         raise ValueError(f"{name} must be [P, T, heads, dh]")
-    ptr = _like(t, name, dtype, tuple(t.shape) if shape is None else shape, device, contiguous=False)
+    ptr = _like(t, name, dtype, t.shape if shape is None else shape, dev, contiguous=False)
+    P, T, heads, dh = t.shape
     if t.is_contiguous():
-        return ptr, t.shape[1] * t.shape[2] * t.shape[3], t.shape[2] * t.shape[3]
+        return ptr, T * heads * dh, heads * dh
     s = t.stride()
-    if (t.shape[3] > 1 and s[3] != 1) or (t.shape[2] > 1 and s[2] != t.shape[3]):
+    if (dh > 1 and s[3] != 1) or (heads > 1 and s[2] != dh):
         raise ValueError(f"{name}: the heads of a token must be contiguous and side by side")
     # a dimension of one element has no stride of its own
-    token = s[1] if t.shape[1] > 1 else t.shape[2] * t.shape[3]
-    return ptr, s[0] if t.shape[0] > 1 else max(s[0], token * t.shape[1]), token
+    token = s[1] if T > 1 else heads * dh
+    return ptr, s[0] if P > 1 else max(s[0], token * T), token
 
 
-def _workspace(workspace, nbytes, device, stream):
+def _workspace(workspace, nbytes, dev, stream):
     """(tensor or None, address, bytes) of a call's workspace; one allocated here is kept from
     reuse until a stream other than the current one has finished with it."""
-    import torch
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = alloc_workspace(nbytes, device)
+        workspace = alloc_workspace(nbytes)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, not {device}")
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on device {dev}")
     return workspace, _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
 def _offsets(cu, name):
-    """Host int32 offsets from a sequence, an array or a CPU tensor."""
-    arr = np.asarray(cu)
-    if arr.ndim != 1 or arr.size < 1 or arr.dtype.kind not in "iu":
-        raise ValueError(f"{name} must be a one-dimensional host array of integers")
-    if arr.dtype != np.int32:
-        if arr.size and (arr.min() < 0 or arr.max() > 2**31 - 1):
+    """(what keeps them, address, count) of host int32 offsets from a sequence, an array or a CPU tensor."""
+    if isinstance(cu, (list, tuple)):
+        try:
+            arr = array.array("i", cu)
+        except OverflowError:
+            raise CaatError(CAAT_ERR_INVALID_ARG, name) from None
+        except TypeError:
+            raise ValueError(f"{name} must be a one-dimensional host array of integers") from None
+        ptr, n = arr.buffer_info()
+    else:
+        arr = np.asarray(cu)
+        if arr.ndim != 1 or arr.dtype.kind not in "iu":
+            raise ValueError(f"{name} must be a one-dimensional host array of integers")
+        if arr.dtype != np.int32 and arr.size and (arr.min() < 0 or arr.max() > 2**31 - 1):
             raise CaatError(CAAT_ERR_INVALID_ARG, name)
-        arr = arr.astype(np.int32)
-    return np.ascontiguousarray(arr)
+        arr = np.ascontiguousarray(arr, dtype=np.int32)
+        ptr, n = arr.__array_interface__["data"][0], arr.size
+    if n < 1:
+        raise ValueError(f"{name} must hold at least one offset")
+    return arr, ptr, n
 
 
 def caat_attn_workspace_size(Tq: int, Tk: int, n_seq: int, P: int, heads_q: int, heads_k: int, dh: int,
                              variant: int = CAAT_VARIANT_ATTN) -> int:
     n = lib().caat_attn_workspace_size(int(Tq), int(Tk), int(n_seq), int(P), int(heads_q), int(heads_k), int(dh),
                                        int(variant))
-    if n == ctypes.c_size_t(-1).value:
+    if n == _SIZE_MAX:
         raise CaatError(CAAT_ERR_INVALID_ARG, "caat_attn_workspace_size")
     return int(n)
+
+
+def _rope_out(o, x, name, dtype, dev):
+    """Address of a rotation's output: contiguous, or the input itself."""
+    if o is x:
+        return x.data_ptr()
+    if o.data_ptr() == x.data_ptr() and o.numel():
+        if o.stride() != x.stride():
+            raise ValueError(f"{name} in place must have its input's shape and strides")
+        return _like(o, name, dtype, x.shape, dev, contiguous=False)
+    return _like(o, name, dtype, x.shape, dev)
 
 
 def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved, backward, mscale, stream, timing):
@@ -687,49 +723,40 @@ def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved,
     first = q if q is not None else k
     if first is None:
         raise ValueError("caat_rope: q and k are both None")
-    dev = first.device
-    _on_current_device(dev)
+    dev = _current(first, "q" if q is not None else "k")
     bf = torch.bfloat16
-    a = RopeArgs()
-    a.P, a.T, a.dh = int(first.shape[0]), int(first.shape[1]), int(first.shape[3])
-
-    def out_ptr(o, x, name):
-        if o is x or (o.data_ptr() == x.data_ptr() and o.stride() == x.stride() and o.shape == x.shape):
-            return _like(o, name, bf, tuple(x.shape), dev, contiguous=False)
-        if o.data_ptr() == x.data_ptr() and o.numel():
-            raise ValueError(f"{name} in place must have its input's shape and strides")
-        return _like(o, name, bf, tuple(x.shape), dev)
-
+    if first.dim() != 4:
+        raise ValueError("q and k must be [P, T, heads, dh]")
+    P, T, heads, dh = first.shape
+    hq = hk = rows = 0
+    q_ptr = k_ptr = v_ptr = qo = ko = vo = slot = None
+    qs = ks = vs = (0, 0)
     if q is not None:
-        a.heads_q = int(q.shape[2])
-        a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
-        a.q_out = out_ptr(q_out, q, "q_out")
+        hq = heads
+        q_ptr, *qs = _heads4(q, "q", bf, dev)
+        qo = _rope_out(q_out, q, "q_out", bf, dev)
     if k is not None:
-        a.heads_k = int(k.shape[2])
-        a.k, a.k_stride_rank, a.k_stride_token = _heads4(k, "k", bf, dev, (a.P, a.T, a.heads_k, a.dh))
+        hk = k.shape[2] if k.dim() == 4 else 0
+        k_ptr, *ks = _heads4(k, "k", bf, dev, (P, T, hk, dh))
         if slots is None:
-            a.k_out = out_ptr(k_out, k, "k_out")
+            ko = _rope_out(k_out, k, "k_out", bf, dev)
         else:
-            a.v, a.v_stride_rank, a.v_stride_token = _heads4(v, "v", bf, dev, (a.P, a.T, a.heads_k, a.dh))
-            a.cache_rows = int(k_out.numel() // (a.P * a.heads_k * a.dh))
-            cache = (a.P, a.cache_rows, a.heads_k, a.dh)
-            slab = tuple(k_out.shape)
-            if k_out.dim() == 5 and slab[:1] + slab[3:] == (a.P, a.heads_k, a.dh):
-                cache = slab
-            a.k_out = _like(k_out, "k_cache", bf, cache, dev)
-            a.v_out = _like(v_out, "v_cache", bf, cache, dev)
-            a.slots = _like(slots, "slots", torch.int64, (a.T,), dev)
-    if positions is not None:
-        a.positions = _like(positions, "positions", torch.int32, (a.T,), dev)
-    freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+            v_ptr, *vs = _heads4(v, "v", bf, dev, (P, T, hk, dh))
+            rows = k_out.numel() // max(P * hk * dh, 1)
+            slab = k_out.shape
+            cache = slab if len(slab) == 5 and slab[0] == P and slab[3:] == (hk, dh) else (P, rows, hk, dh)
+            ko = _like(k_out, "k_cache", bf, cache, dev)
+            vo = _like(v_out, "v_cache", bf, cache, dev)
+            slot = _like(slots, "slots", torch.int64, (T,), dev)
+    pos = None if positions is None else _like(positions, "positions", torch.int32, (T,), dev)
+    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if freq.ndim != 1:
         raise ValueError("inv_freq must be one-dimensional")
-    a.inv_freq, a.rot = freq.ctypes.data, 2 * freq.size
-    a.stream = _stream_ptr(stream)
-    a.timing = timing.handle if timing is not None else None
-    a.mscale = float(mscale)
-    a.flags = (CAAT_ROPE_FLAG_INTERLEAVED if interleaved else 0) | (CAAT_ROPE_FLAG_BACKWARD if backward else 0)
-    _check(lib().caat_rope(ctypes.byref(a)), "caat_rope")
+    a = RopeArgs(q_ptr, k_ptr, v_ptr, qo, ko, vo, pos, slot, freq.__array_interface__["data"][0],
+                 _raw_stream(stream, dev), None if timing is None else timing.handle, T, rows, *qs, *ks, *vs, P, hq, hk, dh,
+                 2 * freq.size, mscale,
+                 (CAAT_ROPE_FLAG_INTERLEAVED if interleaved else 0) | (CAAT_ROPE_FLAG_BACKWARD if backward else 0))
+    _check(lib().caat_rope(a), "caat_rope")
 
 
 def caat_rope(q, k, positions, inv_freq, *, q_out, k_out, interleaved: bool = False, backward: bool = False,
@@ -755,33 +782,32 @@ def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q
     return q_out
 
 
-def _attn_common(a, q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
-    """Fills the arguments the forward and the backward share; returns what must outlive the call."""
+def _attn_tail(q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
+    """What the forward's and the backward's arguments share: (device, what must outlive the call,
+    addresses of q, k and v, the last fields of the structure)."""
     import torch
-    dev = q.device
-    _on_current_device(dev)
+    dev = _current(q, "q")
     bf = torch.bfloat16
-    a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
-    a.P, a.Tq, a.heads_q, a.dh = (int(x) for x in q.shape)
-    a.k, a.k_stride_rank, a.k_stride_token = _heads4(k, "k", bf, dev)
-    a.Tk, a.heads_k = int(k.shape[1]), int(k.shape[2])
-    if k.shape[0] != a.P or k.shape[3] != a.dh:
-        raise ValueError("q and k must have the same ranks and head size")
-    a.v, a.v_stride_rank, a.v_stride_token = _heads4(v, "v", bf, dev, tuple(k.shape))
-    cq = _offsets(cu_q, "cu_q")
-    ck = None if cu_k is None else _offsets(cu_k, "cu_k")
-    if ck is not None and ck.size != cq.size:
-        raise ValueError("cu_q and cu_k must have the same length")
-    a.cu_q, a.n_seq = cq.ctypes.data, cq.size - 1
-    a.cu_k = None if ck is None else ck.ctypes.data
-    a.scale = float(scale) if scale is not None else a.dh ** -0.5
-    a.stream = _stream_ptr(stream)
-    a.timing = timing.handle if timing is not None else None
-    need = lib().caat_attn_workspace_size(a.Tq, a.Tk, a.n_seq, a.P, a.heads_q, a.heads_k, a.dh, variant)
-    if need == ctypes.c_size_t(-1).value:
+    q_ptr, *qs = _heads4(q, "q", bf, dev)
+    P, Tq, hq, dh = q.shape
+    k_ptr, *ks = _heads4(k, "k", bf, dev)
+    _, Tk, hk, _ = k.shape
+    v_ptr, *vs = _heads4(v, "v", bf, dev, (P, Tk, hk, dh))
+    if k.shape != v.shape:
+        raise ValueError("q, k and v must have the same ranks and head size")
+    cq, cq_ptr, n = _offsets(cu_q, "cu_q")
+    ck, ck_ptr = None, None
+    if cu_k is not None:
+        ck, ck_ptr, nk = _offsets(cu_k, "cu_k")
+        if nk != n:
+            raise ValueError("cu_q and cu_k must have the same length")
+    need = lib().caat_attn_workspace_size(Tq, Tk, n - 1, P, hq, hk, dh, variant)
+    if need == _SIZE_MAX:
         need = 0  # sizes the call itself refuses
-    ws, a.workspace, a.ws_bytes = _workspace(workspace, need, dev, stream)
-    return cq, ck, ws
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
+    return dev, (cq, ck, ws), (q_ptr, k_ptr, v_ptr), (
+        cq_ptr, ck_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev), None if timing is None else timing.handle, Tq, Tk, *qs,
+        *ks, *vs, n - 1, P, hq, hk, dh, dh ** -0.5 if scale is None else scale, 0)
 
 
 def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optional[float] = None, workspace=None,
@@ -793,12 +819,11 @@ def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optiona
     query sees the last key); out [P,Tq,heads_q*dh] bf16, the X of caat_rowpar_forward; lse
     [P,heads_q,Tq] fp32, needed by the backward.  scale None: dh ** -0.5."""
     import torch
-    a = AttnArgs()
-    keep = _attn_common(a, q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN, workspace, stream, timing)
-    a.out = _like(out, "out", torch.bfloat16, (a.P, a.Tq, a.heads_q * a.dh), q.device)
-    if lse is not None:
-        a.lse = _like(lse, "lse", torch.float32, (a.P, a.heads_q, a.Tq), q.device)
-    _check(lib().caat_attn_forward(ctypes.byref(a)), "caat_attn_forward")
+    dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN, workspace, stream, timing)
+    P, Tq, hq, dh = q.shape
+    a = AttnArgs(*qkv, _like(out, "out", torch.bfloat16, (P, Tq, hq * dh), dev),
+                 None if lse is None else _like(lse, "lse", torch.float32, (P, hq, Tq), dev), *tail)
+    _check(lib().caat_attn_forward(a), "caat_attn_forward")
     del keep
     return out
 
@@ -808,16 +833,13 @@ def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, 
     """Queues the gradients of caat_attn_forward: dq [P,Tq,heads_q,dh], dk, dv [P,Tk,heads_k,dh] (bf16,
     contiguous) from the forward's inputs, its out and lse, and dout [P,Tq,heads_q*dh]."""
     import torch
-    a = AttnBwdArgs()
-    keep = _attn_common(a, q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN_BWD, workspace, stream, timing)
-    dev, bf = q.device, torch.bfloat16
-    a.out = _like(out, "out", bf, (a.P, a.Tq, a.heads_q * a.dh), dev)
-    a.dout = _like(dout, "dout", bf, (a.P, a.Tq, a.heads_q * a.dh), dev)
-    a.lse = _like(lse, "lse", torch.float32, (a.P, a.heads_q, a.Tq), dev)
-    a.dq = _like(dq, "dq", bf, tuple(q.shape), dev)
-    a.dk = _like(dk, "dk", bf, tuple(k.shape), dev)
-    a.dv = _like(dv, "dv", bf, tuple(k.shape), dev)
-    _check(lib().caat_attn_backward(ctypes.byref(a)), "caat_attn_backward")
+    dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN_BWD, workspace, stream, timing)
+    bf = torch.bfloat16
+    P, Tq, hq, dh = q.shape
+    a = AttnBwdArgs(*qkv, _like(out, "out", bf, (P, Tq, hq * dh), dev), _like(lse, "lse", torch.float32, (P, hq, Tq), dev),
+                    _like(dout, "dout", bf, (P, Tq, hq * dh), dev), _like(dq, "dq", bf, q.shape, dev),
+                    _like(dk, "dk", bf, k.shape, dev), _like(dv, "dv", bf, k.shape, dev), *tail)
+    _check(lib().caat_attn_backward(a), "caat_attn_backward")
     del keep
     return dq, dk, dv
 
@@ -829,28 +851,24 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
     q [P,B,heads_q,dh], caches [P,B,capacity,heads_k,dh] (bf16), lens CUDA int32 [B] (keys of each
     sequence, the new token's included), out [P,B,heads_q*dh]: the X of caat_rowpar_forward."""
     import torch
-    dev, bf = q.device, torch.bfloat16
-    _on_current_device(dev)
-    a = AttnDecodeArgs()
-    a.q, a.q_stride_rank, a.q_stride_token = _heads4(q, "q", bf, dev)
-    a.P, a.B, a.heads_q, a.dh = (int(x) for x in q.shape)
+    bf = torch.bfloat16
+    dev = _current(q, "q")
+    q_ptr, *qs = _heads4(q, "q", bf, dev)
+    P, B, hq, dh = q.shape
     if k_cache.dim() != 5:
         raise ValueError("k_cache must be [P, B, capacity, heads_k, dh]")
-    a.capacity, a.heads_k = int(k_cache.shape[2]), int(k_cache.shape[3])
-    cache = (a.P, a.B, a.capacity, a.heads_k, a.dh)
-    a.k_cache = _like(k_cache, "k_cache", bf, cache, dev)
-    a.v_cache = _like(v_cache, "v_cache", bf, cache, dev)
-    a.lens = _like(lens, "lens", torch.int32, (a.B,), dev)
-    a.out = _like(out, "out", bf, (a.P, a.B, a.heads_q * a.dh), dev)
-    a.scale = float(scale) if scale is not None else a.dh ** -0.5
-    a.stream = _stream_ptr(stream)
-    a.timing = timing.handle if timing is not None else None
-    need = lib().caat_attn_workspace_size(a.B, a.capacity, 0, a.P, a.heads_q, a.heads_k, a.dh,
-                                          CAAT_VARIANT_ATTN_DECODE)
-    if need == ctypes.c_size_t(-1).value:
-        need = 0
-    keep, a.workspace, a.ws_bytes = _workspace(workspace, need, dev, stream)
-    _check(lib().caat_attn_decode(ctypes.byref(a)), "caat_attn_decode")
+    cap, hk = k_cache.shape[2:4]
+    cache = (P, B, cap, hk, dh)
+    k_ptr, v_ptr = _like(k_cache, "k_cache", bf, cache, dev), _like(v_cache, "v_cache", bf, cache, dev)
+    need = lib().caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, CAAT_VARIANT_ATTN_DECODE)
+    if need == _SIZE_MAX:
+        need = 0  # sizes the call itself refuses
+    keep, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
+    a = AttnDecodeArgs(q_ptr, k_ptr, v_ptr, _like(lens, "lens", torch.int32, (B,), dev),
+                       _like(out, "out", bf, (P, B, hq * dh), dev), ws_ptr, ws_bytes, _raw_stream(stream, dev),
+                       None if timing is None else timing.handle, B, cap, *qs, P, hq, hk, dh,
+                       dh ** -0.5 if scale is None else scale, 0)
+    _check(lib().caat_attn_decode(a), "caat_attn_decode")
     del keep
     return out
 

@@ -227,13 +227,16 @@ caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, co
   prm.hq = a->heads_q;
   prm.hk = a->heads_k;
   prm.dh = a->dh;
-  prm.group = group;
-  prm.n_heads = prm.pair_heads ? a->heads_q / 2 : a->heads_q;
-  prm.per_job = a->P * prm.n_heads;
+  const int n_heads = prm.pair_heads ? a->heads_q / 2 : a->heads_q;
+  prm.group_div.set(group);
+  prm.n_heads.set(n_heads);
+  prm.per_job.set(a->P * n_heads);
   prm.scale = a->scale;
   prm.timeout_ns = caat::host::wait_limit_ns();
-  const int64_t grid = int64_t(jobs.size()) * prm.per_job;
-  if (grid > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
+  const int64_t units = int64_t(jobs.size()) * a->P * n_heads;
+  if (units > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
+  prm.n_units = static_cast<int>(units);
+  const int64_t grid = std::min<int64_t>(units, sms);
   CUtensorMap mq, mk, mv;
   if ((s = heads_map(&mq, q, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
   // no keys at all: every row is empty and neither map is used

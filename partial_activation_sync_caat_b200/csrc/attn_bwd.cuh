@@ -61,8 +61,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ BwdAttnParams prm) {
   using Cfg = DqCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (a known address: no registers spent on it)
   uint8_t* sQ = smem;
   uint8_t* sG = smem + Cfg::kTileBytes;
   uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
@@ -81,6 +80,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles would not line up
+    if (threadIdx.x == 0) status_raise(2, 90);
+    return;
+  }
   const int ji = blockIdx.x / prm.per_job;
   const int rh = blockIdx.x - ji * prm.per_job;
   const int rank = rh / prm.hq;
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
   const uint64_t tmo = prm.timeout_ns;
   constexpr uint32_t kDP = KA_TILE, kDQ = 2 * KA_TILE, kDS = 3 * KA_TILE;  // tensor memory columns
 
@@ -152,52 +155,53 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         if (!ok) spin_ns(KA_DRAIN_NS);
       }
     } else if (warp == 8) {
-      if (lane == 0 && n_blk > 0) {
+      if (n_blk > 0) {
+        const uint32_t lead = elect_one();
         constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KA_TILE);
         constexpr uint32_t id_q = idesc_bf16_f32_major(KA_TILE, HD, false, true);
         const uint32_t qa = smem_u32(sQ), ga = smem_u32(sG);
         auto tile = [&](int slot) { return smem_u32(sRing + slot * Cfg::kTileBytes); };
         auto scores = [&](int j) {
-          if (!mbar_wait(&full[Cfg::k_slot(j)], (j / Cfg::kK) & 1, tmo, 112)) return false;
-          if (ragged && j == n_blk - 1 && !mbar_wait(scrubbed, 0, tmo, 113)) return false;
+          if (!warp_wait(&full[Cfg::k_slot(j)], (j / Cfg::kK) & 1, tmo, 112)) return false;
+          if (ragged && j == n_blk - 1 && !warp_wait(scrubbed, 0, tmo, 113)) return false;
           const uint32_t ka = tile(Cfg::k_slot(j)), va = tile(Cfg::v_slot(j));
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
-            umma_bf16(tmem, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), id_s, kk > 0);
+            umma_ss(lead, tmem, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), id_s, kk > 0);
           }
-          if (!mbar_wait(&full[Cfg::v_slot(j)], (j / Cfg::kV) & 1, tmo, 114)) return false;
+          if (!warp_wait(&full[Cfg::v_slot(j)], (j / Cfg::kV) & 1, tmo, 114)) return false;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
-            umma_bf16(tmem + kDP, sw128_kmajor_desc(ga + off), sw128_kmajor_desc(va + off), id_s, kk > 0);
+            umma_ss(lead, tmem + kDP, sw128_kmajor_desc(ga + off), sw128_kmajor_desc(va + off), id_s, kk > 0);
           }
           // also the completion of the product with dS two blocks back, whose buffer comes next
-          umma_commit(sd_full);
-          umma_commit(&empty[Cfg::v_slot(j)]);
+          umma_arrive(lead, sd_full);
+          umma_arrive(lead, &empty[Cfg::v_slot(j)]);
           return true;
         };
-        bool ok = mbar_wait(q_full, 0, tmo, 115) && scores(0);
+        bool ok = warp_wait(q_full, 0, tmo, 115) && scores(0);
         for (int j = 0; j < n_blk && ok; ++j) {
           if (j + 1 < n_blk) {
-            ok = mbar_wait(sd_free, j & 1, tmo, 116);
+            ok = warp_wait(sd_free, j & 1, tmo, 116);
             if (!ok) break;
             tc_fence_after();
             ok = scores(j + 1);
             if (!ok) break;
           }
-          ok = mbar_wait(ds_full, j & 1, tmo, 117);
+          ok = warp_wait(ds_full, j & 1, tmo, 117);
           if (!ok) break;
           tc_fence_after();
           const uint32_t ka = tile(Cfg::k_slot(j));
 #pragma unroll
           for (int kk = 0; kk < KA_TILE / 16; ++kk)
-            umma_bf16_ts(tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, sw128_mnmajor_desc_128(ka + kk * 2048), id_q,
+            umma_ts(lead, tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, sw128_mnmajor_desc_128(ka + kk * 2048), id_q,
                          (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&empty[Cfg::k_slot(j)]);
+          umma_arrive(lead, &empty[Cfg::k_slot(j)]);
         }
-        umma_commit(dq_done);
-        mbar_wait(dq_done, 0, tmo, 118);
+        umma_arrive(lead, dq_done);
+        warp_wait(dq_done, 0, tmo, 118);
       }
     } else if (warp == 10 && ragged) {
       if (warp_wait(k_raw, 0, tmo, 119)) {
@@ -257,7 +261,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         tmem_ld_32x32b_x32(lanes + 64 * w + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * x));
         tmem_ld_32x32b_x32(lanes + kDP + 64 * w + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(g + 32 * x));
       }
-      tmem_wait_ld();
+      tmem_wait_ld(g);
+      tmem_wait_ld(s);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sd_free);
@@ -292,7 +297,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         uint32_t o[32];
         if (n_blk > 0) {
           tmem_ld_32x32b_x32(lanes + kDQ + e, o);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
         }
         if (mine) {
 #pragma unroll
@@ -343,8 +348,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ BwdAttnParams prm) {
   using Cfg = DkvCfg<HD>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];  // (a known address: no registers spent on it)
   uint8_t* sK = smem;
   uint8_t* sV = smem + Cfg::kTileBytes;
   uint8_t* sQ = smem + 2 * Cfg::kTileBytes;
@@ -362,6 +366,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles would not line up
+    if (threadIdx.x == 0) status_raise(2, 90);
+    return;
+  }
   const int ji = blockIdx.x / prm.per_job;
   int rest = blockIdx.x - ji * prm.per_job;
   const int split = rest % prm.splits;
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
   const uint64_t tmo = prm.timeout_ns;
   constexpr uint32_t kDV = 4 * KB2_QT, kDK = 4 * KB2_QT + HD;
 
@@ -433,29 +441,30 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         if (!ok) spin_ns(KA_DRAIN_NS);
       }
     } else if (warp == 8) {
-      if (lane == 0 && n > 0) {
+      if (n > 0) {
+        const uint32_t lead = elect_one();
         constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KB2_QT);
         constexpr uint32_t id_g = idesc_bf16_f32_major(KA_TILE, HD, false, true);
         const uint32_t ka = smem_u32(sK), va = smem_u32(sV);
         auto scores = [&](int i) {
           const int st = i % Cfg::kStages;
-          if (!mbar_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 132)) return false;
+          if (!warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 132)) return false;
           const uint32_t qa = smem_u32(sQ + st * Cfg::kQBytes), ga = smem_u32(sG + st * Cfg::kQBytes);
           const uint32_t d = tmem + (i & 1) * 2 * KB2_QT;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
-            umma_bf16(d, sw128_kmajor_desc(ka + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
+            umma_ss(lead, d, sw128_kmajor_desc(ka + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
                       sw128_kmajor_desc(qa + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
-            umma_bf16(d + KB2_QT, sw128_kmajor_desc(va + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
+            umma_ss(lead, d + KB2_QT, sw128_kmajor_desc(va + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
                       sw128_kmajor_desc(ga + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
-          umma_commit(&sd_full[i & 1]);
+          umma_arrive(lead, &sd_full[i & 1]);
           return true;
         };
-        bool ok = mbar_wait(kv_full, 0, tmo, 133) && scores(0) && (n < 2 || scores(1));
+        bool ok = warp_wait(kv_full, 0, tmo, 133) && scores(0) && (n < 2 || scores(1));
         for (int i = 0; i < n && ok; ++i) {
-          ok = mbar_wait(&pd_full[i & 1], (i >> 1) & 1, tmo, 134);
+          ok = warp_wait(&pd_full[i & 1], (i >> 1) & 1, tmo, 134);
           if (!ok) break;
           tc_fence_after();
           const int st = i % Cfg::kStages;
@@ -463,16 +472,16 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
           const uint32_t a = tmem + (i & 1) * 2 * KB2_QT;
 #pragma unroll
           for (int kk = 0; kk < KB2_QT / 16; ++kk)
-            umma_bf16_ts(tmem + kDV, a + 8 * kk, sw128_mnmajor_desc(ga + kk * 2048), id_g, (i > 0 || kk > 0) ? 1u : 0u);
+            umma_ts(lead, tmem + kDV, a + 8 * kk, sw128_mnmajor_desc(ga + kk * 2048), id_g, (i > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
           for (int kk = 0; kk < KB2_QT / 16; ++kk)
-            umma_bf16_ts(tmem + kDK, a + KB2_QT + 8 * kk, sw128_mnmajor_desc(qa + kk * 2048), id_g,
+            umma_ts(lead, tmem + kDK, a + KB2_QT + 8 * kk, sw128_mnmajor_desc(qa + kk * 2048), id_g,
                          (i > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&empty[st]);
+          umma_arrive(lead, &empty[st]);
           if (i + 2 < n) ok = scores(i + 2);
         }
-        umma_commit(done);
-        mbar_wait(done, 0, tmo, 135);
+        umma_arrive(lead, done);
+        warp_wait(done, 0, tmo, 135);
       }
     } else if (warp == 10) {
       for (int i = 0; i < n; ++i) {
@@ -528,7 +537,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         tmem_ld_32x32b_x32(base + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * x));
         tmem_ld_32x32b_x32(base + KB2_QT + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(g + 32 * x));
       }
-      tmem_wait_ld();
+      tmem_wait_ld(g);
+      tmem_wait_ld(s);
       const int h = (it0 + i) / nt, x0 = ((it0 + i) - h * nt) * KB2_QT;
       const int lo = row + job.first - x0;    // the key is seen from this query of the step on
       const int hi = job.rows - x0;           // queries of the step
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         uint32_t o[32];
         if (n > 0) {
           tmem_ld_32x32b_x32(lanes + (w ? kDK : kDV) + x, o);
-          tmem_wait_ld();
+          tmem_wait_ld(o);
         }
         if (mine) {
 #pragma unroll

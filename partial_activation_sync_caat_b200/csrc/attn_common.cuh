@@ -31,6 +31,22 @@ struct AttnJobChunk {
   AttnJob job[KA_UPLOAD_JOBS];
 };
 
+// Division by a launch constant (n < 2^31) as a high product and a shift: with l = ceil(log2 d) and
+// mul = floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(n, mul) + n) >> l.  (The compiler would otherwise
+// keep each divisor's reciprocal in registers across the kernels' main loops.)
+struct FastDiv {
+  uint32_t d, mul, shift;
+  void set(uint32_t div) {
+    d = div;
+    shift = 0;
+    while ((uint64_t(1) << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - div)) / div + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+};
+
 __global__ void attn_upload_kernel(AttnJob* dst, int n, const __grid_constant__ AttnJobChunk c) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = c.job[i];
 }
@@ -44,15 +60,72 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* map, uin
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: A bf16, its rows in the lanes and two K neighbours per column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// One lane of the warp.  The MMA warps run their loops with all lanes, so that descriptors and addresses
+// stay in uniform registers, and predicate the MMA instructions themselves with this.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, by the lane with lead != 0.
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
       : "memory");
+}
+
+// The same with A in tensor memory: bf16, its rows in the lanes and two K neighbours per column.
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+__device__ __forceinline__ void umma_arrive(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+
+// Waits for the thread's tensor-memory loads into r.  The loads write their registers behind the
+// compiler's back until then: listing them here keeps every use of them below the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
 // The thread's lane of 32 columns.
@@ -111,6 +184,63 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 2^x of two values without the special-function unit: x = n + f with n the nearest whole number, 2^f
+// by the polynomial of degree 5 that interpolates it at the 6 Chebyshev nodes of [-1/2, 1/2] (off by
+// 1.0e-7 relative, 2.2e-7 = 2^-22 as evaluated in fp32), and 2^n put together in the exponent field.
+// x below -126.5 gives 0, x is at most 126, NaN stays NaN.
+__device__ __forceinline__ uint64_t ex2_poly_f32x2(uint64_t x) {
+  float a, b;
+  unpack_f32x2(x, a, b);
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(a));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(b));
+  const uint64_t c = pack_f32x2(a, b);
+  const uint64_t t = add_f32x2(c, pack_f32x2(12582912.f, 12582912.f));  // 1.5 2^23: n in the low bits
+  const uint64_t n = add_f32x2(t, pack_f32x2(-12582912.f, -12582912.f));
+  const uint64_t f = fma_f32x2(n, pack_f32x2(-1.f, -1.f), c);
+  uint64_t r = fma_f32x2(f, pack_f32x2(0.0013390863364571618f, 0.0013390863364571618f),
+                         pack_f32x2(0.00967603191832481f, 0.00967603191832481f));
+  r = fma_f32x2(r, f, pack_f32x2(0.05550357114219401f, 0.05550357114219401f));
+  r = fma_f32x2(r, f, pack_f32x2(0.2402210748530825f, 0.2402210748530825f));
+  r = fma_f32x2(r, f, pack_f32x2(0.6931471880262285f, 0.6931471880262285f));
+  r = fma_f32x2(r, f, pack_f32x2(1.0000000754548972f, 1.0000000754548972f));
+  unpack_f32x2(t, a, b);
+  const uint32_t ea = (__float_as_uint(a) << 23) + 0x3F800000u, eb = (__float_as_uint(b) << 23) + 0x3F800000u;
+  return mul_f32x2(r, pack_f32x2(__uint_as_float(ea), __uint_as_float(eb)));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The long part of a wait, kept out of the loops: their code should stay short.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t tmo, int site) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 1;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    if (__all_sync(0xFFFFFFFFu, done)) return true;
+    if ((n & 63u) == 0u) {
+      if (__any_sync(0xFFFFFFFFu, status_poll() != 0)) return false;
+      if (__any_sync(0xFFFFFFFFu, globaltimer_ns() - t0 > tmo)) {
+        status_raise(4, site);
+        return false;
+      }
+    }
+  }
+}
+
+// Bounded wait of a whole warp (uniform result).
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, uint64_t tmo, int site) {
+  if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+  return wait_long(smem_u32(bar), parity, tmo, site);
 }
 
 // Warp-uniform bounded wait of all lanes.

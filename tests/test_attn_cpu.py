@@ -190,14 +190,18 @@ def test_binding_refuses_cpu_tensors_and_odd_layouts(L):
     with pytest.raises(ValueError):
         C.caat_rope(None, None, None, freq, q_out=None, k_out=None)
     with pytest.raises(ValueError):
-        C._heads4(q.transpose(2, 3), "q", torch.bfloat16, q.device)
+        C._heads4(q.transpose(2, 3), "q", torch.bfloat16, -1)
     with pytest.raises(ValueError):
-        C._heads4(q[..., ::2], "q", torch.bfloat16, q.device)
+        C._heads4(q[..., ::2], "q", torch.bfloat16, -1)
     with pytest.raises(TypeError):
-        C._heads4(q.float(), "q", torch.bfloat16, q.device)
-    assert C._heads4(q[:, 1:, :1], "q", torch.bfloat16, q.device)[1:] == (4 * 128, 128)
-    for bad in ([[0, 1]], [0.0, 1.0], []):
+        C._heads4(q.float(), "q", torch.bfloat16, -1)
+    assert C._heads4(q[:, 1:, :1], "q", torch.bfloat16, -1)[1:] == (4 * 128, 128)
+    for good in ([0, 4], (0, 4), np.array([0, 4]), np.array([9, 0, 4, 7], dtype=np.int32)[1:3], torch.tensor([0, 4])):
+        keep, ptr, n = C._offsets(good, "cu_q")
+        assert n == 2 and list((ctypes.c_int32 * 2).from_address(ptr)) == [0, 4] and keep is not None
+    for bad in ([[0, 1]], [0.0, 1.0], [], np.array([[0, 1]]), np.array([0.0, 1.0]), "01"):
         with pytest.raises(ValueError):
             C._offsets(bad, "cu_q")
-    with pytest.raises(C.CaatError):
-        C._offsets([0, 2**31], "cu_q")
+    for big in ([0, 2**31], np.array([0, 2**31])):
+        with pytest.raises(C.CaatError):
+            C._offsets(big, "cu_q")
