@@ -46,7 +46,7 @@ struct DqCfg {
   static constexpr int kK = HD == 128 ? 3 : 4;
   static constexpr int kV = HD == 128 ? 2 : 3;
   static constexpr int kSlots = kK + kV;
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + 2 * KA_TILE * 4 + 512;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + KA_TILE * 4 + 512;
   static __device__ __forceinline__ int k_slot(int j) { return j % kK; }
   static __device__ __forceinline__ int v_slot(int j) { return kK + j % kV; }
 };
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   uint8_t* sQ = smem;
   uint8_t* sG = smem + Cfg::kTileBytes;
   uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
-  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 2 * KA_TILE);
+  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + KA_TILE);
   uint64_t* q_full = bars;
   uint64_t* full = q_full + 1;             // [slots]
   uint64_t* empty = full + Cfg::kSlots;    // [slots]
@@ -159,49 +159,57 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         const uint32_t lead = elect_one();
         constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KA_TILE);
         constexpr uint32_t id_q = idesc_bf16_f32_major(KA_TILE, HD, false, true);
-        const uint32_t qa = smem_u32(sQ), ga = smem_u32(sG);
-        auto tile = [&](int slot) { return smem_u32(sRing + slot * Cfg::kTileBytes); };
+        constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4;
+        const uint64_t dQ = sw128_kmajor_desc(smem_u32(sQ)), dG = sw128_kmajor_desc(smem_u32(sG));
+        const uint64_t dR = sw128_kmajor_desc(smem_u32(sRing)), dRt = sw128_mnmajor_desc_128(smem_u32(sRing));
+        int ks = 0, vs = 0;            // slots of the next K and V block, and their phases
+        uint32_t kp = 0, vp = 0;
         auto scores = [&](int j) {
-          if (!warp_wait(&full[Cfg::k_slot(j)], (j / Cfg::kK) & 1, tmo, 112)) return false;
-          if (ragged && j == n_blk - 1 && !warp_wait(scrubbed, 0, tmo, 113)) return false;
-          const uint32_t ka = tile(Cfg::k_slot(j)), va = tile(Cfg::v_slot(j));
+          if (!lane_wait(&full[ks], kp, tmo, 112)) return false;
+          if (ragged && j == n_blk - 1 && !lane_wait(scrubbed, 0, tmo, 113)) return false;
+          const uint64_t dk = dR + ks * kTile16;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
-            umma_ss(lead, tmem, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), id_s, kk > 0);
+            const uint32_t off = ((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4;
+            umma_ss(lead, tmem, dQ + off, dk + off, id_s, kk > 0);
           }
-          if (!warp_wait(&full[Cfg::v_slot(j)], (j / Cfg::kV) & 1, tmo, 114)) return false;
+          if (!lane_wait(&full[Cfg::kK + vs], vp, tmo, 114)) return false;
+          const uint64_t dv = dR + (Cfg::kK + vs) * kTile16;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32;
-            umma_ss(lead, tmem + kDP, sw128_kmajor_desc(ga + off), sw128_kmajor_desc(va + off), id_s, kk > 0);
+            const uint32_t off = ((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4;
+            umma_ss(lead, tmem + kDP, dG + off, dv + off, id_s, kk > 0);
           }
           // also the completion of the product with dS two blocks back, whose buffer comes next
           umma_arrive(lead, sd_full);
-          umma_arrive(lead, &empty[Cfg::v_slot(j)]);
+          umma_arrive(lead, &empty[Cfg::kK + vs]);
+          if (++ks == Cfg::kK) { ks = 0; kp ^= 1; }
+          if (++vs == Cfg::kV) { vs = 0; vp ^= 1; }
           return true;
         };
-        bool ok = warp_wait(q_full, 0, tmo, 115) && scores(0);
+        bool ok = lane_wait(q_full, 0, tmo, 115) && scores(0);
+        int kq = 0;  // slot of the block whose dS comes next
         for (int j = 0; j < n_blk && ok; ++j) {
           if (j + 1 < n_blk) {
-            ok = warp_wait(sd_free, j & 1, tmo, 116);
+            ok = lane_wait(sd_free, j & 1, tmo, 116);
             if (!ok) break;
             tc_fence_after();
             ok = scores(j + 1);
             if (!ok) break;
           }
-          ok = warp_wait(ds_full, j & 1, tmo, 117);
+          ok = lane_wait(ds_full, j & 1, tmo, 117);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ka = tile(Cfg::k_slot(j));
+          const uint64_t dk = dRt + kq * kTile16;
 #pragma unroll
           for (int kk = 0; kk < KA_TILE / 16; ++kk)
-            umma_ts(lead, tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, sw128_mnmajor_desc_128(ka + kk * 2048), id_q,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-          umma_arrive(lead, &empty[Cfg::k_slot(j)]);
+            umma_ts(lead, tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, dk + (kk * 2048 >> 4), id_q,
+                    (j > 0 || kk > 0) ? 1u : 0u);
+          umma_arrive(lead, &empty[kq]);
+          if (++kq == Cfg::kK) kq = 0;
         }
         umma_arrive(lead, dq_done);
-        warp_wait(dq_done, 0, tmo, 118);
+        lane_wait(dq_done, 0, tmo, 118);
       }
     } else if (warp == 10 && ragged) {
       if (warp_wait(k_raw, 0, tmo, 119)) {
@@ -225,26 +233,35 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const int64_t grow = job.q0 + row;
     const int64_t orow = ((rank * prm.Tq + grow) * prm.hq + head) * prm.dh;
     const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
-    // D: each thread sums half of its row
-    float part = 0.f;
-    if (mine) {
+    // D: 16 lanes a row, a warp 16 rows (a row a lane, the loads touched 32 rows each and took 12,000
+    // clocks; 16,000 rows a CTA apart they miss every cache)
+    {
+      uint4 o[8], g[8];
+      const int e = 8 * (lane & 15);
 #pragma unroll
-      for (int x = 0; x < HD / 16; ++x) {
-        const int e = w * (HD / 2) + 8 * x;
-        if (e < prm.dh) {
-          const uint4 a = ld_nc_v4(prm.out + orow + e), b = ld_nc_v4(prm.dout + orow + e);
-          const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
+      for (int i = 0; i < 8; ++i) {
+        const int r = 16 * warp + 2 * i + (lane >> 4);
+        const bool in = r < job.rows && e < prm.dh;
+        const int64_t off = ((rank * prm.Tq + job.q0 + r) * prm.hq + head) * prm.dh + e;
+        o[i] = in ? ld_nc_v4(prm.out + off) : make_uint4(0, 0, 0, 0);
+        g[i] = in ? ld_nc_v4(prm.dout + off) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
-            part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
-          }
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t wa[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, wb[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+        float part = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
+          part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
         }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+        if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
       }
     }
-    sD[w * KA_TILE + row] = part;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float D = sD[row] + sD[KA_TILE + row];
+    const float D = sD[row];
     if (mine && w == 0) prm.D[srow] = D;
     const float c = prm.scale * KA_LOG2E;
     const float nl = mine ? -prm.lse[srow] * KA_LOG2E : 0.f;
@@ -291,29 +308,28 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     if (ok && n_blk > 0) ok = warp_wait(dq_done, 0, tmo, 121);
     tc_fence_after();
     if (ok) {
+      // every product is done: the Q tile's place serves to turn the rows
+      const int e = w * (HD / 2);
+      uint4 v[HD / 16];
 #pragma unroll
       for (int x = 0; x < HD / 2; x += 32) {
-        const int e = w * (HD / 2) + x;
         uint32_t o[32];
         if (n_blk > 0) {
-          tmem_ld_32x32b_x32(lanes + kDQ + e, o);
+          tmem_ld_32x32b_x32(lanes + kDQ + e + x, o);
           tmem_wait_ld(o);
         }
-        if (mine) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (e + 8 * y < prm.dh) {
-              uint32_t v[4];
+        for (int y = 0; y < 4; ++y) {
+          uint32_t u[4];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float a = __uint_as_float(o[8 * y + 2 * u]) * prm.scale, b = __uint_as_float(o[8 * y + 2 * u + 1]) * prm.scale;
-                v[u] = n_blk > 0 ? pack_bf16x2(a, b) : 0u;
-              }
-              st_v4(prm.dq + orow + e + 8 * y, make_uint4(v[0], v[1], v[2], v[3]));
-            }
-          }
+          for (int z = 0; z < 4; ++z)
+            u[z] = n_blk > 0 ? pack_bf16x2(__uint_as_float(o[8 * y + 2 * z]) * prm.scale, __uint_as_float(o[8 * y + 2 * z + 1]) * prm.scale) : 0u;
+          v[x / 8 + y] = make_uint4(u[0], u[1], u[2], u[3]);
         }
       }
+      const int64_t base = ((rank * prm.Tq + job.q0 + q * 32) * prm.hq + head) * prm.dh + e;
+      warp_store_rows(sQ + warp * (32 * HD), v, reinterpret_cast<uint8_t*>(prm.dq + base), int64_t(prm.hq) * prm.dh * 2,
+                      job.rows - q * 32, (prm.dh - e) / 8, lane);
     }
   }
 
@@ -445,43 +461,51 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         const uint32_t lead = elect_one();
         constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KB2_QT);
         constexpr uint32_t id_g = idesc_bf16_f32_major(KA_TILE, HD, false, true);
-        const uint32_t ka = smem_u32(sK), va = smem_u32(sV);
-        auto scores = [&](int i) {
-          const int st = i % Cfg::kStages;
-          if (!warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 132)) return false;
-          const uint32_t qa = smem_u32(sQ + st * Cfg::kQBytes), ga = smem_u32(sG + st * Cfg::kQBytes);
-          const uint32_t d = tmem + (i & 1) * 2 * KB2_QT;
+        constexpr uint32_t kQ16 = Cfg::kQBytes >> 4;
+        const uint64_t dK = sw128_kmajor_desc(smem_u32(sK)), dV = sw128_kmajor_desc(smem_u32(sV));
+        const uint64_t dQ = sw128_kmajor_desc(smem_u32(sQ)), dG = sw128_kmajor_desc(smem_u32(sG));
+        const uint64_t dQt = sw128_mnmajor_desc(smem_u32(sQ)), dGt = sw128_mnmajor_desc(smem_u32(sG));
+        int ss = 0, st = 0;  // stages of the next scores and of the next sums
+        uint32_t sp = 0;
+        auto scores = [&](uint32_t buf) {
+          if (!lane_wait(&full[ss], sp, tmo, 132)) return false;
+          const uint64_t q = dQ + ss * kQ16, g = dG + ss * kQ16;
+          const uint32_t d = tmem + buf * 2 * KB2_QT;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
-            umma_ss(lead, d, sw128_kmajor_desc(ka + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
-                      sw128_kmajor_desc(qa + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
+            umma_ss(lead, d, dK + (((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4),
+                    q + (((kk >> 2) * Cfg::kQBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk)
-            umma_ss(lead, d + KB2_QT, sw128_kmajor_desc(va + (kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32),
-                      sw128_kmajor_desc(ga + (kk >> 2) * Cfg::kQBox + (kk & 3) * 32), id_s, kk > 0);
-          umma_arrive(lead, &sd_full[i & 1]);
+            umma_ss(lead, d + KB2_QT, dV + (((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4),
+                    g + (((kk >> 2) * Cfg::kQBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
+          umma_arrive(lead, &sd_full[buf]);
+          if (++ss == Cfg::kStages) { ss = 0; sp ^= 1; }
           return true;
         };
-        bool ok = warp_wait(kv_full, 0, tmo, 133) && scores(0) && (n < 2 || scores(1));
-        for (int i = 0; i < n && ok; ++i) {
-          ok = warp_wait(&pd_full[i & 1], (i >> 1) & 1, tmo, 134);
-          if (!ok) break;
-          tc_fence_after();
-          const int st = i % Cfg::kStages;
-          const uint32_t qa = smem_u32(sQ + st * Cfg::kQBytes), ga = smem_u32(sG + st * Cfg::kQBytes);
-          const uint32_t a = tmem + (i & 1) * 2 * KB2_QT;
+        bool ok = lane_wait(kv_full, 0, tmo, 133);
+#pragma unroll 1
+        for (int i = -2; i < n && ok; ++i) {
+          const uint32_t buf = i & 1;
+          if (i >= 0) {
+            ok = lane_wait(&pd_full[buf], (i >> 1) & 1, tmo, 134);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t q = dQt + st * kQ16, g = dGt + st * kQ16;
+            const uint32_t a = tmem + buf * 2 * KB2_QT;
 #pragma unroll
-          for (int kk = 0; kk < KB2_QT / 16; ++kk)
-            umma_ts(lead, tmem + kDV, a + 8 * kk, sw128_mnmajor_desc(ga + kk * 2048), id_g, (i > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < KB2_QT / 16; ++kk)
+              umma_ts(lead, tmem + kDV, a + 8 * kk, g + (kk * 2048 >> 4), id_g, (i > 0 || kk > 0) ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < KB2_QT / 16; ++kk)
-            umma_ts(lead, tmem + kDK, a + KB2_QT + 8 * kk, sw128_mnmajor_desc(qa + kk * 2048), id_g,
-                         (i > 0 || kk > 0) ? 1u : 0u);
-          umma_arrive(lead, &empty[st]);
-          if (i + 2 < n) ok = scores(i + 2);
+            for (int kk = 0; kk < KB2_QT / 16; ++kk)
+              umma_ts(lead, tmem + kDK, a + KB2_QT + 8 * kk, q + (kk * 2048 >> 4), id_g, (i > 0 || kk > 0) ? 1u : 0u);
+            umma_arrive(lead, &empty[st]);
+            if (++st == Cfg::kStages) st = 0;
+          }
+          if (i + 2 < n) ok = scores(buf);
         }
         umma_arrive(lead, done);
-        warp_wait(done, 0, tmo, 135);
+        lane_wait(done, 0, tmo, 135);
       }
     } else if (warp == 10) {
       for (int i = 0; i < n; ++i) {
@@ -525,6 +549,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const float c = prm.scale * KA_LOG2E;
     const uint64_t c2 = pack_f32x2(c, c);
     bool ok = true;
+    int x0 = n > 0 ? ((it0 + w) % nt) * KB2_QT : 0;  // the step's first query
     for (int i = w; i < n; i += 2) {
       const int st = i % Cfg::kStages;
       ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 137) && warp_wait(&sd_full[w], (i >> 1) & 1, tmo, 138);
@@ -539,7 +564,6 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       }
       tmem_wait_ld(g);
       tmem_wait_ld(s);
-      const int h = (it0 + i) / nt, x0 = ((it0 + i) - h * nt) * KB2_QT;
       const int lo = row + job.first - x0;    // the key is seen from this query of the step on
       const int hi = job.rows - x0;           // queries of the step
       const bool cut = hi < KB2_QT || q * 32 + 31 + job.first > x0;
@@ -574,40 +598,44 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pd_full[w]);
+      x0 += 2 * KB2_QT;
+      while (x0 >= nt * KB2_QT) x0 -= nt * KB2_QT;  // the next head
     }
     if (ok && n > 0) ok = warp_wait(done, 0, tmo, 139);
     tc_fence_after();
     if (ok) {
       // warps 0-3 store dV, 4-7 dK
-      const bool mine = row < job.k_rows;
       const float f = w ? prm.scale : 1.f;
-      const int64_t krow = ((rank * prm.Tk + job.k0 + row) * prm.hk + kvh) * prm.dh;
-      const int64_t all = prm.P * prm.Tk * prm.hk * prm.dh;
-      __nv_bfloat16* dst = (w ? prm.dk : prm.dv) + krow;
+      const int64_t krow = ((rank * prm.Tk + job.k0 + q * 32) * prm.hk + kvh) * prm.dh;
+      const int64_t all = prm.P * prm.Tk * prm.hk * prm.dh, stride = int64_t(prm.hk) * prm.dh;
+      const int rows = job.k_rows - q * 32;
       float* pdst = prm.part + (w * prm.splits + split) * all + krow;
-#pragma unroll
+      __nv_bfloat16* dst = (w ? prm.dk : prm.dv) + krow;
+      uint8_t* patch = sQ + warp * 4096;  // every product is done
+#pragma unroll 1
       for (int x = 0; x < HD; x += 32) {
         uint32_t o[32];
         if (n > 0) {
           tmem_ld_32x32b_x32(lanes + (w ? kDK : kDV) + x, o);
           tmem_wait_ld(o);
         }
-        if (mine) {
+#pragma unroll
+        for (int y = 0; y < 32; ++y) o[y] = n > 0 ? __float_as_uint(__uint_as_float(o[y]) * f) : 0u;
+        if (prm.splits > 1) {
+          uint4 v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) v[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          warp_store_rows(patch, v, reinterpret_cast<uint8_t*>(pdst + x), stride * 4, rows, (prm.dh - x) / 4, lane);
+        } else {
+          uint4 v[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            if (x + 8 * y < prm.dh) {
-              float v[8];
+            uint32_t u[4];
 #pragma unroll
-              for (int u = 0; u < 8; ++u) v[u] = n > 0 ? __uint_as_float(o[8 * y + u]) * f : 0.f;
-              if (prm.splits > 1) {
-                *reinterpret_cast<float4*>(pdst + x + 8 * y) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(pdst + x + 8 * y + 4) = make_float4(v[4], v[5], v[6], v[7]);
-              } else {
-                st_v4(dst + x + 8 * y, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                                  pack_bf16x2(v[6], v[7])));
-              }
-            }
+            for (int z = 0; z < 4; ++z) u[z] = pack_bf16x2(__uint_as_float(o[8 * y + 2 * z]), __uint_as_float(o[8 * y + 2 * z + 1]));
+            v[y] = make_uint4(u[0], u[1], u[2], u[3]);
           }
+          warp_store_rows(patch, v, reinterpret_cast<uint8_t*>(dst + x), stride * 2, rows, (prm.dh - x) / 8, lane);
         }
       }
     }

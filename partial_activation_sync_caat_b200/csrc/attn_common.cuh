@@ -216,6 +216,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Stores a warp's 32 rows of kChunks 16-byte pieces, lane = row, through a patch of shared memory (32
+// kChunks 16 bytes), so that neighbouring lanes store neighbouring pieces of a row: a row a lane, each
+// store instruction touches 32 rows and takes as many trips.  `rows` rows and `chunks` pieces exist.
+template <int kChunks>
+__device__ __forceinline__ void warp_store_rows(uint8_t* patch, const uint4 (&v)[kChunks], uint8_t* dst, int64_t stride,
+                                                int rows, int chunks, int lane) {
+  constexpr int kMask = kChunks < 8 ? kChunks - 1 : 7;
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) *reinterpret_cast<uint4*>(patch + (lane * kChunks + (c ^ (lane & kMask))) * 16) = v[c];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int r = (i * 32 + lane) / kChunks, c = (i * 32 + lane) % kChunks;
+    if (r < rows && c < chunks)
+      st_v4(dst + r * stride + c * 16, *reinterpret_cast<const uint4*>(patch + (r * kChunks + (c ^ (r & kMask))) * 16));
+  }
+  __syncwarp();
+}
+
 // The long part of a wait, kept out of the loops: their code should stay short.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint64_t tmo, int site) {
   const uint64_t t0 = globaltimer_ns();
