@@ -231,7 +231,6 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const bool mine = row < job.rows;
     const int64_t grow = job.q0 + row;
-    const int64_t orow = ((rank * prm.Tq + grow) * prm.hq + head) * prm.dh;
     const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
     // D: 16 lanes a row, a warp 16 rows (a row a lane, the loads touched 32 rows each and took 12,000
     // clocks; 16,000 rows a CTA apart they miss every cache)
@@ -264,7 +263,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const float D = sD[row];
     if (mine && w == 0) prm.D[srow] = D;
     const float c = prm.scale * KA_LOG2E;
-    const float nl = mine ? -prm.lse[srow] * KA_LOG2E : 0.f;
+    float nl = mine ? -prm.lse[srow] * KA_LOG2E : 0.f;
+    if (nl == INFINITY) nl = 0.f;  // a row that sees no key: all its scores are masked
     const uint64_t c2 = pack_f32x2(c, c), nl2 = pack_f32x2(nl, nl), nd2 = pack_f32x2(-D, -D);
     const int vis = job.first + row;
     bool ok = true;
@@ -285,6 +285,14 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       if (lane == 0) mbar_arrive(sd_free);
       const int seen = vis - j * KA_TILE - 64 * w;
       const bool cut = job.first + q * 32 - j * KA_TILE - 64 * w < 64;
+      if (cut) {
+        // unseen: s = -inf makes p = 0, and dP = 0 keeps dS = p (dP - D) from being 0 times a NaN
+#pragma unroll
+        for (int y = 0; y < 64; ++y) {
+          s[y] = y < seen ? s[y] : 0xFF800000u;
+          g[y] = y < seen ? g[y] : 0u;
+        }
+      }
       uint32_t p[32];
 #pragma unroll
       for (int y = 0; y < 32; ++y) {
@@ -293,10 +301,6 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         unpack_f32x2(mul_f32x2(pack_f32x2(ex2(a), ex2(b)),
                                add_f32x2(pack_f32x2(__uint_as_float(g[2 * y]), __uint_as_float(g[2 * y + 1])), nd2)),
                      x0, x1);
-        if (cut) {
-          x0 = 2 * y < seen ? x0 : 0.f;
-          x1 = 2 * y + 1 < seen ? x1 : 0.f;
-        }
         p[y] = pack_bf16x2(x0, x1);
       }
       tmem_st_32x32b_x32(lanes + kDS + (j & 1) * 64 + 32 * w, p);
@@ -567,6 +571,15 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       const int lo = row + job.first - x0;    // the key is seen from this query of the step on
       const int hi = job.rows - x0;           // queries of the step
       const bool cut = hi < KB2_QT || q * 32 + 31 + job.first > x0;
+      if (cut) {
+        // unseen: s = -inf makes p = 0, and dP = 0 keeps dS = p (dP - D) from being 0 times a NaN
+#pragma unroll
+        for (int y = 0; y < KB2_QT; ++y) {
+          const bool see = y >= lo && y < hi;
+          s[y] = see ? s[y] : 0xFF800000u;
+          g[y] = see ? g[y] : 0u;
+        }
+      }
       const float4* l = reinterpret_cast<const float4*>(sL + st * 2 * KB2_QT);
       uint32_t pp[32], pd[32];
 #pragma unroll
@@ -579,14 +592,6 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         for (int u = 0; u < 4; ++u) a[u] = ex2(a[u]);
         unpack_f32x2(mul_f32x2(pack_f32x2(a[0], a[1]), add_f32x2(pack_f32x2(__uint_as_float(g[4 * y]), __uint_as_float(g[4 * y + 1])), pack_f32x2(nd.x, nd.y))), d[0], d[1]);
         unpack_f32x2(mul_f32x2(pack_f32x2(a[2], a[3]), add_f32x2(pack_f32x2(__uint_as_float(g[4 * y + 2]), __uint_as_float(g[4 * y + 3])), pack_f32x2(nd.z, nd.w))), d[2], d[3]);
-        if (cut) {
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const bool see = 4 * y + u >= lo && 4 * y + u < hi;
-            a[u] = see ? a[u] : 0.f;
-            d[u] = see ? d[u] : 0.f;
-          }
-        }
         pp[2 * y] = pack_bf16x2(a[0], a[1]);
         pp[2 * y + 1] = pack_bf16x2(a[2], a[3]);
         pd[2 * y] = pack_bf16x2(d[0], d[1]);
