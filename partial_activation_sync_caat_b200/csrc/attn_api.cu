@@ -41,6 +41,8 @@ namespace {
 
 using caat::host::Recorder;
 
+constexpr size_t kDecodeCounters = 2048;  // 4 bytes per CTA
+static_assert(caat::KD_CTAS * 4 <= kDecodeCounters, "one counter per CTA");
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a buffer, rows of a cache
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -434,10 +436,17 @@ caat_status caat_rope(const caat_rope_args* a) {
     prm.turns[j] = (a->flags & CAAT_ROPE_FLAG_BACKWARD ? -kInvTwoPi : kInvTwoPi) * a->inv_freq[j];
   Recorder rec;
   rec.begin(a->timing, a->stream);
-  if (inter)
-    caat::rope_kernel<true><<<static_cast<unsigned>(a->T), caat::KR_THREADS, 0, a->stream>>>(prm);
-  else
-    caat::rope_kernel<false><<<static_cast<unsigned>(a->T), caat::KR_THREADS, 0, a->stream>>>(prm);
+  const int64_t rows = int64_t(a->P) * (prm.q.heads + prm.k.heads + prm.v.heads);
+  const int64_t items = rows * (a->dh / 8);  // at most: vectors of a token
+  // Four items a thread keep enough loads in flight for many tokens; for few, one a thread spreads them
+  // over more SMs.
+  const bool few = a->T * ((items + 1023) / 1024) < 4 * int64_t(sms);
+  const int per_cta = caat::KR_THREADS * (few ? 1 : 4);
+  const unsigned gy = static_cast<unsigned>((items + per_cta - 1) / per_cta);
+  const unsigned gx = static_cast<unsigned>(std::min<int64_t>(a->T, std::max<int64_t>(1, (8 * int64_t(sms) + gy - 1) / gy)));
+  auto kernel = inter ? (few ? caat::rope_kernel<true, 1> : caat::rope_kernel<true, 4>)
+                      : (few ? caat::rope_kernel<false, 1> : caat::rope_kernel<false, 4>);
+  kernel<<<dim3(gx, gy), caat::KR_THREADS, 0, a->stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
   return CAAT_OK;
@@ -451,7 +460,7 @@ size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int he
     case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
     case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : bwd_layout(Tq, Tk, n_seq, P, heads_q, heads_k, dh).total;
     case CAAT_VARIANT_ATTN_DECODE:
-      return align256(size_t(caat::KD_CTAS) * 2 * std::min(heads_q / heads_k, 16) * (dh + 2) * 4);
+      return kDecodeCounters + align256(size_t(caat::KD_CTAS) * 2 * std::min(heads_q / heads_k, 16) * (dh + 2) * 4);
   }
   return SIZE_MAX;
 }
@@ -570,7 +579,8 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   p.v = reinterpret_cast<const __nv_bfloat16*>(a->v_cache);
   p.lens = a->lens;
   p.out = reinterpret_cast<__nv_bfloat16*>(a->out);
-  p.part = static_cast<float*>(a->workspace);
+  p.count = static_cast<unsigned int*>(a->workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kDecodeCounters);
   p.q_rank = q.rank;
   p.q_tok = q.tok;
   p.B = a->B;
@@ -585,35 +595,31 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   p.G = a->P * a->heads_k * p.n_gb;
   p.scale = a->scale;
   const int HD = a->dh <= 64 ? 64 : 128;
-  const int stage = 4 * 2 * 16 * HD * 2, index = static_cast<int>(a->B + 5) * 4;
+  const int tile = 4 * caat::kd_keys(HD);
+  const int stage = tile * 2 * HD * 2, index = static_cast<int>(a->B + 5) * 4;
   const int merge = 4 * p.rows * (HD + 2) * 4;
   p.stages = std::min(5, (caat::KD_SMEM - merge - index) / stage);
   const int bytes = p.stages * stage + merge + index;
-  const int64_t most = int64_t(p.G) * a->B * ((a->capacity + caat::KD_TILE - 1) / caat::KD_TILE);
+  const int64_t most = int64_t(p.G) * a->B * ((a->capacity + tile - 1) / tile);
   const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(caat::KD_CTAS, most)));
   Recorder rec;
   rec.begin(a->timing, a->stream);
-  if (HD == 64)
-    caat::attn_decode_kernel<64><<<ctas, caat::KD_THREADS, bytes, a->stream>>>(p);
-  else
-    caat::attn_decode_kernel<128><<<ctas, caat::KD_THREADS, bytes, a->stream>>>(p);
+  caat::attn_decode_clear_kernel<<<1, caat::KD_CTAS, 0, a->stream>>>(p.count);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(caat::KD_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = a->stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = HD == 64 ? cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<64>, p)
+                                 : cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<128>, p);
+  if (e != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
-  if (ctas > 1) {
-    // launched while the first kernel still runs; it waits for it before reading the partial results
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(ctas - 1, 1, 1);
-    cfg.blockDim = dim3(caat::KD_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = index;
-    cfg.stream = a->stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, caat::attn_decode_join_kernel, p, ctas) != cudaSuccess) return CAAT_ERR_CUDA;
-    rec.after_kernel(a->stream);
-  }
   return CAAT_OK;
 }
 

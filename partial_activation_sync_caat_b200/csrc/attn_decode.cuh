@@ -1,12 +1,15 @@
 // attn_decode.cuh - one new token per sequence against its cache, on every rank.
 //
 // Every byte of K and V is used once, so the read rate of the memory bounds it.  The work is the list of
-// 64-key tiles of all (sequence, rank, key head) segments; it is cut evenly over a fixed number of
+// tiles (64 keys, of dh <= 64: 128) of all (sequence, rank, key head) segments; it is cut evenly over a fixed number of
 // CTAs, whatever the lengths, so that one long sequence and many short ones alike keep all SMs
-// reading.  A segment cut between CTAs leaves fp32 partial results (maximum, sum, sums of p v) that a
-// second kernel joins, in the order of the CTAs.
+// reading.  A segment cut between CTAs leaves fp32 partial results (maximum, sum, sums of p v); the
+// CTA that finishes the last of them joins them, in the order of the CTAs, so results do not change from
+// run to run.  The counters it goes by are cleared by a kernel of one block that this one is launched
+// behind without waiting (programmatic dependent launch: it waits before it counts).  A second kernel for that, launched
+// early and waiting, measured 12 us more per call.
 //
-// Inside a CTA each of the 4 warps owns 16 of a tile's keys and a ring of its own, filled with
+// Inside a CTA each of the 4 warps owns a quarter of a tile's keys and a ring of its own, filled with
 // 16-byte asynchronous copies: no block-wide waits until a segment ends, when the warps' running
 // maxima, sums and products are merged through shared memory.  Up to 16 query heads of the group share
 // the tile as the 16 rows of the MMA (legacy mma.sync: the products are a small part of the time even
@@ -21,7 +24,8 @@
 namespace caat {
 
 constexpr int KD_THREADS = 128;
-constexpr int KD_TILE = 64;        // keys of a tile: 16 per warp
+// Keys of a tile per warp (4 warps): 32 KiB of K and V a tile at either width.
+__host__ __device__ constexpr int kd_keys(int HD) { return HD == 64 ? 32 : 16; }
 constexpr int KD_CTAS = 296;       // two per SM
 constexpr int KD_MAX_B = 4096;
 constexpr int KD_SMEM = 113 * 1024;
@@ -32,6 +36,7 @@ struct DecodeAttnParams {
   const __nv_bfloat16* v;
   const int32_t* lens;
   __nv_bfloat16* out;          // [P, B, hq, dh]
+  unsigned int* count;         // [CTAs], zero: parts of the segment that began in that CTA and are done
   float* part;                 // [CTAs][2][rows][dh + 2]: sums of p v, maximum (scaled, base 2), sum of p
   int64_t q_rank, q_tok;
   int64_t B, capacity;
@@ -44,14 +49,14 @@ struct DecodeAttnParams {
 };
 
 // pre[b] = tiles of the sequences before b, pre[B] = all of them.  A length outside the cache counts as 0.
-__device__ __forceinline__ void decode_prefix(const DecodeAttnParams& prm, int* pre, int* warp_sums) {
+__device__ __forceinline__ void decode_prefix(const DecodeAttnParams& prm, int tile, int* pre, int* warp_sums) {
   const int B = static_cast<int>(prm.B);
   const int per = (B + KD_THREADS - 1) / KD_THREADS;
   const int b0 = threadIdx.x * per;
   int sum = 0;
   for (int b = b0; b < min(b0 + per, B); ++b) {
     const int len = __ldg(prm.lens + b);
-    sum += (len > 0 && len <= prm.capacity) ? (len + KD_TILE - 1) / KD_TILE : 0;
+    sum += (len > 0 && len <= prm.capacity) ? (len + tile - 1) / tile : 0;
   }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int inc = sum;
@@ -67,10 +72,27 @@ __device__ __forceinline__ void decode_prefix(const DecodeAttnParams& prm, int* 
   for (int b = b0; b < min(b0 + per, B); ++b) {
     pre[b] = at;
     const int len = __ldg(prm.lens + b);
-    at += (len > 0 && len <= prm.capacity) ? (len + KD_TILE - 1) / KD_TILE : 0;
+    at += (len > 0 && len <= prm.capacity) ? (len + tile - 1) / tile : 0;
   }
   if (b0 < B && b0 + per >= B) pre[B] = at;
   __syncthreads();
+}
+
+// The list is dealt in runs of equal length, the first `extra` CTAs one tile more.
+struct DecodeDeal {
+  int64_t each;
+  int extra;
+  __device__ __forceinline__ DecodeDeal(int64_t total, int ctas) : each(total / ctas), extra(static_cast<int>(total - each * ctas)) {}
+  __device__ __forceinline__ int64_t begin(int cta) const { return cta * each + min(cta, extra); }
+  __device__ __forceinline__ int owner(int64_t item) const {
+    const int64_t longer = extra * (each + 1);
+    return static_cast<int>(item < longer ? item / (each + 1) : extra + (item - longer) / each);
+  }
+};
+
+__global__ void __launch_bounds__(KD_CTAS) attn_decode_clear_kernel(unsigned int* count) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  count[threadIdx.x] = 0;
 }
 
 // A tile of the work list: sequence, segment of the sequence, tile of the segment.
@@ -123,21 +145,64 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Joins the parts of a segment that CTAs z0..z1 left; z0, where it begins, in its slot 1, the others in
+// their slot 0.  A warp a row: its lanes fetch the parts' maxima and sums side by side.
+__device__ __noinline__ void decode_join(const DecodeAttnParams& prm, int z0, int z1, int b, int rank, int head0, int rows,
+                                         int warp, int lane) {
+  const int64_t stride = int64_t(prm.rows) * (prm.dh + 2);
+  for (int r = warp; r < rows; r += KD_THREADS / 32) {
+    const float* p0 = prm.part + r * (prm.dh + 2);
+    auto part = [&](int z) { return p0 + (2 * int64_t(z) + (z == z0)) * stride; };
+    float M = -INFINITY;
+    for (int z = z0 + lane; z <= z1; z += 32) M = fmaxf(M, __ldcg(part(z) + prm.dh));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int z = z0; z <= z1; z += 32) {  // in the order of the CTAs
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (z + lane <= z1) ml = __ldcg(reinterpret_cast<const float2*>(part(z + lane) + prm.dh));
+      const float f = ex2(ml.x - base), fl = f * ml.y;
+      const int n = min(32, z1 + 1 - z);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
+        L += __shfl_sync(0xFFFFFFFFu, fl, i);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (2 * lane + 64 * e < prm.dh) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(part(z + i) + 2 * lane + 64 * e));
+            o[2 * e] = fmaf(fi, v.x, o[2 * e]);
+            o[2 * e + 1] = fmaf(fi, v.y, o[2 * e + 1]);
+          }
+      }
+    }
+    const float inv = 1.f / L;
+    __nv_bfloat16* dst = prm.out + ((rank * prm.B + b) * prm.hq + head0 + r) * prm.dh + 2 * lane;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (2 * lane + 64 * e < prm.dh) *reinterpret_cast<uint32_t*>(dst + 64 * e) = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid_constant__ DecodeAttnParams prm) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int kKeys = kd_keys(HD);           // a warp's keys of a tile
+  constexpr int kTile = 4 * kKeys;
   constexpr int kRow = HD * 2;                 // bytes of a key's row in shared memory
-  constexpr int kStage = 2 * 16 * kRow;        // a warp's 16 keys of K and of V
+  constexpr int kStage = 2 * kKeys * kRow;     // a warp's keys of K and of V
   constexpr int kChunks = HD / 8;
+  constexpr int kStep = 32 / kChunks;          // keys that one copy instruction of the warp covers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem_raw + warp * prm.stages * kStage;
   float* merge = reinterpret_cast<float*>(smem_raw + 4 * prm.stages * kStage);  // [4][rows][HD]
   float* ml = merge + 4 * prm.rows * HD;                                        // [4][rows][2]
   int* pre = reinterpret_cast<int*>(ml + 4 * prm.rows * 2);                     // [B + 1]
   int* warp_sums = pre + prm.B + 1;
+  __shared__ int last_part;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  decode_prefix(prm, pre, warp_sums);
+  decode_prefix(prm, kTile, pre, warp_sums);
   // sequences without keys
   for (int64_t b = blockIdx.x; b < prm.B; b += gridDim.x) {
     if (pre[b + 1] != pre[b]) continue;
@@ -147,9 +212,12 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       for (int i = threadIdx.x; i < n; i += KD_THREADS)
         st_v4(prm.out + (r * prm.B + b) * prm.hq * prm.dh + 8 * i, make_uint4(0, 0, 0, 0));
   }
-  const int64_t total = int64_t(pre[prm.B]) * prm.G;
-  const int64_t i0 = total * blockIdx.x / gridDim.x, i1 = total * (blockIdx.x + 1) / gridDim.x;
-  if (i0 == i1) return;
+  const DecodeDeal deal(int64_t(pre[prm.B]) * prm.G, gridDim.x);
+  const int64_t i0 = deal.begin(blockIdx.x), i1 = deal.begin(blockIdx.x + 1);
+  if (i0 == i1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   DecodeCursor ld, at;
   ld.seek(prm, pre, i0);
@@ -162,26 +230,40 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
     rank = x / prm.hk;
     kvh = x - rank * prm.hk;
   };
+  // Each lane copies one 16-byte piece of every kStep-th key; its pointers and the keys left behind its
+  // first one are carried from tile to tile and set up again only where a segment begins.
+  const int my_key = warp * kKeys + lane / kChunks, my_chunk = lane % kChunks;
+  const bool my_part = my_chunk * 8 < prm.dh;
+  const int64_t tok = int64_t(prm.hk) * prm.dh;
+  const __nv_bfloat16 *kp = prm.k, *vp = prm.v;
+  int ahead = 0;
+  bool fresh_ld = true;
   auto load = [&](int stage) {
     if (todo > 0) {
-      int rank, kvh, gb;
-      split_g(ld.g, rank, kvh, gb);
-      const int key0 = ld.t * KD_TILE + warp * 16;
-      const int live = __ldg(prm.lens + ld.b) - key0;
-      const int64_t tok = int64_t(prm.hk) * prm.dh;
-      const int64_t base = ((rank * prm.B + ld.b) * prm.capacity + key0) * tok + int64_t(kvh) * prm.dh;
+      if (fresh_ld) {
+        int rank, kvh, gb;
+        split_g(ld.g, rank, kvh, gb);
+        const int key = ld.t * kTile + my_key;
+        const int64_t off = ((rank * prm.B + ld.b) * prm.capacity + key) * tok + int64_t(kvh) * prm.dh + my_chunk * 8;
+        kp = prm.k + off;
+        vp = prm.v + off;
+        ahead = my_part ? __ldg(prm.lens + ld.b) - key : 0;
+        fresh_ld = false;
+      }
       const uint32_t dst = smem_u32(ring + stage * kStage);
 #pragma unroll
-      for (int i = 0; i < 16 * kChunks / 32; ++i) {
-        const int x = i * 32 + lane;
-        const int r = x / kChunks, ch = x % kChunks;
-        const bool in = r < live && ch * 8 < prm.dh;
-        const int64_t off = in ? base + r * tok + ch * 8 : 0;
-        const uint32_t d = dst + r * kRow + ((ch ^ (r & 7)) << 4);
-        cp_async_16(d, prm.k + off, in ? 16 : 0);
-        cp_async_16(d + 16 * kRow, prm.v + off, in ? 16 : 0);
+      for (int i = 0; i < kKeys / kStep; ++i) {
+        const int r = i * kStep + lane / kChunks;
+        const bool in = i * kStep < ahead;
+        const uint32_t d = dst + r * kRow + ((my_chunk ^ (r & 7)) << 4);
+        cp_async_16(d, in ? kp + i * kStep * tok : prm.k, in ? 16 : 0);
+        cp_async_16(d + kKeys * kRow, in ? vp + i * kStep * tok : prm.v, in ? 16 : 0);
       }
+      kp += kTile * tok;
+      vp += kTile * tok;
+      ahead -= kTile;
       --todo;
+      fresh_ld = ld.t + 1 == ld.tiles;
       ld.next(prm, pre);
     }
     cp_async_commit();
@@ -192,15 +274,16 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
   const int r0 = lane >> 2;  // the thread's rows: r0, r0 + 8
   uint32_t qa[HD / 16][4];
   float o[HD / 8][4];
-  float m[2], l[2];
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  int rank = 0, kvh = 0, gb = 0, rows = 0, head0 = 0, len = 0;
   bool fresh = true;
   int stage = 0, ld_stage = prm.stages - 1;
   for (int64_t left = i1 - i0; left > 0; --left) {
-    int rank, kvh, gb;
-    split_g(at.g, rank, kvh, gb);
-    const int rows = min(prm.group - 16 * gb, 16);
-    const int head0 = kvh * prm.group + 16 * gb;
     if (fresh) {
+      split_g(at.g, rank, kvh, gb);
+      rows = min(prm.group - 16 * gb, 16);
+      head0 = kvh * prm.group + 16 * gb;
+      len = __ldg(prm.lens + at.b);
       const __nv_bfloat16* q = prm.q + rank * prm.q_rank + at.b * prm.q_tok + int64_t(head0) * prm.dh;
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
@@ -226,25 +309,30 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       default: cp_async_wait<4>(); break;
     }
     __syncwarp();
-    const uint32_t ks = smem_u32(ring + stage * kStage), vs = ks + 16 * kRow;
-    const int live = __ldg(prm.lens + at.b) - (at.t * KD_TILE + warp * 16);
+    const uint32_t ks = smem_u32(ring + stage * kStage), vs = ks + kKeys * kRow;
+    const int live = len - (at.t * kTile + warp * kKeys);
     if (live > 0) {
-      float s[2][4] = {};
+      float s[kKeys / 8][4] = {};
       const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;  // ldmatrix row and chunk of the lane
 #pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk) {
-        uint32_t b[4];
-        ldmatrix_x4(ks + kr * kRow + (((2 * kk + kc) ^ (kr & 7)) << 4), b);
-        mma_16816(s[0], qa[kk], b[0], b[1]);
-        mma_16816(s[1], qa[kk], b[2], b[3]);
-      }
+      for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x) {
+          uint32_t b[4];
+          ldmatrix_x4(ks + (16 * x + kr) * kRow + (((2 * kk + kc) ^ (kr & 7)) << 4), b);
+          mma_16816(s[2 * x], qa[kk], b[0], b[1]);
+          mma_16816(s[2 * x + 1], qa[kk], b[2], b[3]);
+        }
       float top[2] = {m[0], m[1]};
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < kKeys / 8; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = 8 * x + 2 * (lane & 3) + (e & 1);
-          s[x][e] = key < live ? s[x][e] * c : -INFINITY;
+          s[x][e] *= c;
+          if (live < kKeys) {
+            const int key = 8 * x + 2 * (lane & 3) + (e & 1);
+            s[x][e] = key < live ? s[x][e] : -INFINITY;
+          }
           top[e >> 1] = fmaxf(top[e >> 1], s[x][e]);
         }
 #pragma unroll
@@ -252,7 +340,8 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
         top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
         top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
       }
-      if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1])) {
+      // the maximum only moves when exceeded by 2^8: p stays below 256, the quotient is the same
+      if (__any_sync(0xFFFFFFFFu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float f = top[e] > m[e] ? ex2(m[e] - top[e]) : 1.f;
@@ -265,24 +354,26 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
           }
         }
       }
-      uint32_t pa[4];
+      uint32_t pa[kKeys / 16][4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < kKeys / 8; ++x)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float base = m[e] == -INFINITY ? 0.f : m[e];
           const float p0 = ex2(s[x][2 * e] - base), p1 = ex2(s[x][2 * e + 1] - base);
           l[e] += p0 + p1;
-          pa[2 * x + e] = pack_bf16x2(p0, p1);
+          pa[x >> 1][2 * (x & 1) + e] = pack_bf16x2(p0, p1);
         }
       const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
 #pragma unroll
-      for (int x = 0; x < HD / 16; ++x) {
-        uint32_t b[4];
-        ldmatrix_x4_trans(vs + vr * kRow + (((2 * x + vc) ^ (vr & 7)) << 4), b);
-        mma_16816(o[2 * x], pa, b[0], b[1]);
-        mma_16816(o[2 * x + 1], pa, b[2], b[3]);
-      }
+      for (int y = 0; y < kKeys / 16; ++y)
+#pragma unroll
+        for (int x = 0; x < HD / 16; ++x) {
+          uint32_t b[4];
+          ldmatrix_x4_trans(vs + (16 * y + vr) * kRow + (((2 * x + vc) ^ (vr & 7)) << 4), b);
+          mma_16816(o[2 * x], pa[y], b[0], b[1]);
+          mma_16816(o[2 * x + 1], pa[y], b[2], b[3]);
+        }
     }
     __syncwarp();
     stage = stage + 1 == prm.stages ? 0 : stage + 1;
@@ -310,8 +401,9 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       const bool starts_here = left + at.t <= i1 - i0;  // the segment's first tile is this CTA's
       const bool complete = ends && starts_here;
       float* part = prm.part + (int64_t(blockIdx.x) * 2 + (starts_here ? 1 : 0)) * prm.rows * (prm.dh + 2);
-      for (int i = threadIdx.x; i < rows * (prm.dh / 2); i += KD_THREADS) {
-        const int r = i / (prm.dh / 2), d = 2 * (i - r * (prm.dh / 2));
+      for (int i = threadIdx.x; i < rows * (HD / 2); i += KD_THREADS) {
+        const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
+        if (d >= prm.dh) continue;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[(w * prm.rows + r) * 2]);
@@ -331,65 +423,28 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
               pack_bf16x2(x0 * inv, x1 * inv);
         } else {
           float* p = part + r * (prm.dh + 2);
-          p[d] = x0;
-          p[d + 1] = x1;
-          if (d == 0) {
-            p[prm.dh] = M;
-            p[prm.dh + 1] = L;
-          }
+          *reinterpret_cast<float2*>(p + d) = make_float2(x0, x1);
+          if (d == 0) *reinterpret_cast<float2*>(p + prm.dh) = make_float2(M, L);
         }
       }
       __syncthreads();
+      if (!complete) {
+        const int64_t begin = i1 - left - at.t;
+        const int z0 = starts_here ? blockIdx.x : deal.owner(begin), z1 = deal.owner(begin + at.tiles - 1);
+        if (threadIdx.x == 0) {
+          __threadfence();
+          asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are cleared
+          last_part = atomicAdd(prm.count + z0, 1u) == static_cast<unsigned int>(z1 - z0);
+          __threadfence();
+        }
+        __syncthreads();
+        if (last_part) decode_join(prm, z0, z1, at.b, rank, head0, rows, warp, lane);
+      }
       fresh = true;
     }
     at.next(prm, pre);
   }
-}
-
-// Joins the segments that a boundary between CTAs cuts: block c - 1 takes the segment that boundary c is
-// the first to cut.
-__global__ void __launch_bounds__(KD_THREADS) attn_decode_join_kernel(const __grid_constant__ DecodeAttnParams prm, int ctas) {
-  extern __shared__ int pre[];
-  int* warp_sums = pre + prm.B + 1;
-  decode_prefix(prm, pre, warp_sums);
-  // every block waits for the partial results, so that this kernel never ends before the first one
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x + 1;
-  const int64_t total = int64_t(pre[prm.B]) * prm.G;
-  const int64_t cut = total * c / ctas, before = total * (c - 1) / ctas;
-  if (cut == before || cut >= total) return;  // CTA c - 1 had nothing, or nothing follows
-  DecodeCursor at;
-  at.seek(prm, pre, cut);
-  const int64_t begin = cut - at.t, end = begin + at.tiles;
-  if (at.t == 0 || begin < before) return;
-  int last = c;  // the last CTA with tiles of the segment
-  while (total * (last + 1) / ctas < end) ++last;
-  const int gb = at.g % prm.n_gb, x = at.g / prm.n_gb, rank = x / prm.hk, kvh = x - rank * prm.hk;
-  const int rows = min(prm.group - 16 * gb, 16);
-  const int64_t stride = int64_t(prm.rows) * (prm.dh + 2);
-  // with fewer tiles than CTAs some CTAs have none and left nothing
-  auto had_tiles = [&](int z) { return total * (z + 1) / ctas > total * z / ctas; };
-  for (int i = threadIdx.x; i < rows * (prm.dh / 2); i += KD_THREADS) {
-    const int r = i / (prm.dh / 2), d = 2 * (i - r * (prm.dh / 2));
-    const float* p0 = prm.part + r * (prm.dh + 2);
-    // the CTA that begins the segment left it in its slot 1, the others in their slot 0
-    float M = -INFINITY;
-    for (int z = c - 1; z <= last; ++z)
-      if (had_tiles(z)) M = fmaxf(M, p0[(2 * int64_t(z) + (z == c - 1)) * stride + prm.dh]);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, x0 = 0.f, x1 = 0.f;
-    for (int z = c - 1; z <= last; ++z) {
-      if (!had_tiles(z)) continue;
-      const float* p = p0 + (2 * int64_t(z) + (z == c - 1)) * stride;
-      const float f = ex2(p[prm.dh] - base);
-      L = fmaf(f, p[prm.dh + 1], L);
-      x0 = fmaf(f, p[d], x0);
-      x1 = fmaf(f, p[d + 1], x1);
-    }
-    const float inv = 1.f / L;
-    *reinterpret_cast<uint32_t*>(prm.out + ((rank * prm.B + at.b) * prm.hq + kvh * prm.group + 16 * gb + r) * prm.dh + d) =
-        pack_bf16x2(x0 * inv, x1 * inv);
-  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block, so that the clearing never outlives this kernel)
 }
 
 }  // namespace caat
