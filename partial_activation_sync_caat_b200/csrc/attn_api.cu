@@ -436,16 +436,16 @@ caat_status caat_rope(const caat_rope_args* a) {
     prm.turns[j] = (a->flags & CAAT_ROPE_FLAG_BACKWARD ? -kInvTwoPi : kInvTwoPi) * a->inv_freq[j];
   Recorder rec;
   rec.begin(a->timing, a->stream);
-  const int64_t rows = int64_t(a->P) * (prm.q.heads + prm.k.heads + prm.v.heads);
-  const int64_t items = rows * (a->dh / 8);  // at most: vectors of a token
-  // Four items a thread keep enough loads in flight for many tokens; for few, one a thread spreads them
-  // over more SMs.
-  const bool few = a->T * ((items + 1023) / 1024) < 4 * int64_t(sms);
-  const int per_cta = caat::KR_THREADS * (few ? 1 : 4);
+  const int per_head = a->rot / (inter ? 8 : 16) + (a->dh - a->rot) / 8;
+  const int64_t items = int64_t(a->P) * ((prm.q.heads + prm.k.heads) * per_head + prm.v.heads * (a->dh / 8));
+  // Two items a thread keep more loads in flight for many tokens; for few, one a thread spreads them over
+  // more SMs.
+  const bool few = a->T * ((items + 511) / 512) < 4 * int64_t(sms);
+  const int per_cta = caat::KR_THREADS * (few ? 1 : 2);
   const unsigned gy = static_cast<unsigned>((items + per_cta - 1) / per_cta);
-  const unsigned gx = static_cast<unsigned>(std::min<int64_t>(a->T, std::max<int64_t>(1, (8 * int64_t(sms) + gy - 1) / gy)));
-  auto kernel = inter ? (few ? caat::rope_kernel<true, 1> : caat::rope_kernel<true, 4>)
-                      : (few ? caat::rope_kernel<false, 1> : caat::rope_kernel<false, 4>);
+  const unsigned gx = static_cast<unsigned>(std::min<int64_t>(a->T, std::max<int64_t>(1, (caat::KR_CTAS * int64_t(sms) + gy - 1) / gy)));
+  auto kernel = inter ? (few ? caat::rope_kernel<true, 1> : caat::rope_kernel<true, 2>)
+                      : (few ? caat::rope_kernel<false, 1> : caat::rope_kernel<false, 2>);
   kernel<<<dim3(gx, gy), caat::KR_THREADS, 0, a->stream>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);

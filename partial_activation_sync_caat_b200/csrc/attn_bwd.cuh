@@ -94,7 +94,23 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   const int n_blk = (m_seen + KA_TILE - 1) / KA_TILE;
   const bool ragged = (m_seen & (KA_TILE - 1)) != 0;  // the last block reaches past the sequence's keys
 
-  if (threadIdx.x == 0) {
+  // The TMA warp sets up the barriers and sends the first loads off before the block meets; the elementwise
+  // warps' loads for D go out before that, too.
+  const uint64_t pol_q = policy_evict_first(), pol_kv = policy_evict_last();
+  auto load_kv = [&](int i) {
+    const int j = i >> 1;
+    const int slot = (i & 1) ? Cfg::v_slot(j) : Cfg::k_slot(j);
+    uint64_t* bar = &full[slot];
+    if (ragged && i == 2 * (n_blk - 1)) {
+      bar = k_raw;
+      mbar_arrive(&full[slot]);
+    }
+    mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+    for (int b = 0; b < Cfg::kBoxes; ++b)
+      tma_load_4d(sRing + slot * Cfg::kTileBytes + b * KA_BOX_BYTES, (i & 1) ? &tmV : &tmK, bar, 64 * b, kvh,
+                  job.k0 + j * KA_TILE, rank, pol_kv);
+  };
+  if (threadIdx.x == 9 * 32) {
     mbar_init(q_full, 1);
     for (int s = 0; s < Cfg::kSlots; ++s) {
       mbar_init(&full[s], 1);
@@ -107,10 +123,25 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     mbar_init(scrubbed, 1);
     mbar_init(dq_done, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmG);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    if (n_blk > 0) {
+      mbar_arrive_expect_tx(q_full, 2 * Cfg::kTileBytes);
+      for (int b = 0; b < Cfg::kBoxes; ++b) tma_load_4d(sQ + b * KA_BOX_BYTES, &tmQ, q_full, 64 * b, head, job.q0, rank, pol_q);
+      load_kv(0);
+      for (int b = 0; b < Cfg::kBoxes; ++b) tma_load_4d(sG + b * KA_BOX_BYTES, &tmG, q_full, 64 * b, head, job.q0, rank, pol_q);
+      load_kv(1);
+    }
+  }
+  uint4 d_o[8], d_g[8];  // 16 lanes a row, a warp 16 rows
+  if (warp < 8) {
+    const int e = 8 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 16 * warp + 2 * i + (lane >> 4);
+      const bool in = r < job.rows && e < prm.dh;
+      const int64_t off = ((rank * prm.Tq + job.q0 + r) * prm.hq + head) * prm.dh + e;
+      d_o[i] = in ? ld_nc_v4(prm.out + off) : make_uint4(0, 0, 0, 0);
+      d_g[i] = in ? ld_nc_v4(prm.dout + off) : make_uint4(0, 0, 0, 0);
+    }
   }
   if (warp == 8) {
     tmem_alloc(tmem_holder, 512);
@@ -127,30 +158,12 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 9) {
       if (lane == 0 && n_blk > 0) {
-        const uint64_t pol_q = policy_evict_first();
-        const uint64_t pol_kv = policy_evict_last();
-        mbar_arrive_expect_tx(q_full, 2 * Cfg::kTileBytes);
-        for (int b = 0; b < Cfg::kBoxes; ++b) {
-          tma_load_4d(sQ + b * KA_BOX_BYTES, &tmQ, q_full, 64 * b, head, job.q0, rank, pol_q);
-          tma_load_4d(sG + b * KA_BOX_BYTES, &tmG, q_full, 64 * b, head, job.q0, rank, pol_q);
-        }
         bool ok = true;
-        for (int i = 0; i < 2 * n_blk && ok; ++i) {
+        for (int i = 2; i < 2 * n_blk && ok; ++i) {
           const int j = i >> 1;
           const int slot = (i & 1) ? Cfg::v_slot(j) : Cfg::k_slot(j);
-          if (!mbar_wait(&empty[slot], ((j / ((i & 1) ? Cfg::kV : Cfg::kK)) & 1) ^ 1, tmo, 111)) {
-            ok = false;
-            break;
-          }
-          uint64_t* bar = &full[slot];
-          if (ragged && i == 2 * (n_blk - 1)) {
-            bar = k_raw;
-            mbar_arrive(&full[slot]);
-          }
-          mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
-          for (int b = 0; b < Cfg::kBoxes; ++b)
-            tma_load_4d(sRing + slot * Cfg::kTileBytes + b * KA_BOX_BYTES, (i & 1) ? &tmV : &tmK, bar, 64 * b, kvh,
-                        job.k0 + j * KA_TILE, rank, pol_kv);
+          ok = mbar_wait(&empty[slot], ((j / ((i & 1) ? Cfg::kV : Cfg::kK)) & 1) ^ 1, tmo, 111);
+          if (ok) load_kv(i);
         }
         if (!ok) spin_ns(KA_DRAIN_NS);
       }
@@ -232,32 +245,19 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const bool mine = row < job.rows;
     const int64_t grow = job.q0 + row;
     const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
-    // D: 16 lanes a row, a warp 16 rows (a row a lane, the loads touched 32 rows each and took 12,000
-    // clocks; 16,000 rows a CTA apart they miss every cache)
-    {
-      uint4 o[8], g[8];
-      const int e = 8 * (lane & 15);
+    // D: a row a lane, the loads touched 32 rows each and took 12,000 clocks
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 16 * warp + 2 * i + (lane >> 4);
-        const bool in = r < job.rows && e < prm.dh;
-        const int64_t off = ((rank * prm.Tq + job.q0 + r) * prm.hq + head) * prm.dh + e;
-        o[i] = in ? ld_nc_v4(prm.out + off) : make_uint4(0, 0, 0, 0);
-        g[i] = in ? ld_nc_v4(prm.dout + off) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t wa[4] = {d_o[i].x, d_o[i].y, d_o[i].z, d_o[i].w}, wb[4] = {d_g[i].x, d_g[i].y, d_g[i].z, d_g[i].w};
+      float part = 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
+        part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t wa[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, wb[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
-        float part = 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
-          part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
-        }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
-        if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
-      }
+      for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+      if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const float D = sD[row];
@@ -402,7 +402,18 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   const int it0 = static_cast<int>(int64_t(total) * split / prm.splits);
   const int n = static_cast<int>(int64_t(total) * (split + 1) / prm.splits) - it0;
 
-  if (threadIdx.x == 0) {
+  const uint64_t pol_kv = policy_evict_first(), pol_q = policy_evict_last();
+  auto load_q = [&](int i) {
+    const int st = i % Cfg::kStages, h = (it0 + i) / nt, x = (it0 + i) - h * nt;
+    mbar_arrive_expect_tx(&raw[st], 2 * Cfg::kQBytes);
+    for (int b = 0; b < Cfg::kBoxes; ++b) {
+      tma_load_4d(sQ + st * Cfg::kQBytes + b * Cfg::kQBox, &tmQ, &raw[st], 64 * b, kvh * prm.group + h,
+                  job.q0 + x * KB2_QT, rank, pol_q);
+      tma_load_4d(sG + st * Cfg::kQBytes + b * Cfg::kQBox, &tmG, &raw[st], 64 * b, kvh * prm.group + h,
+                  job.q0 + x * KB2_QT, rank, pol_q);
+    }
+  };
+  if (threadIdx.x == 9 * 32) {  // the TMA warp sends the first loads off before the block meets
     mbar_init(kv_full, 1);
     for (int s = 0; s < Cfg::kStages; ++s) {
       mbar_init(&raw[s], 1);
@@ -415,10 +426,12 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     }
     mbar_init(done, 1);
     fence_mbar_init();
-    tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmG);
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    if (n > 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * Cfg::kTileBytes);
+      for (int b = 0; b < Cfg::kBoxes; ++b) tma_load_4d(sK + b * KA_BOX_BYTES, &tmK, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
+      load_q(0);
+      for (int b = 0; b < Cfg::kBoxes; ++b) tma_load_4d(sV + b * KA_BOX_BYTES, &tmV, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
+    }
   }
   if (warp == 8) {
     tmem_alloc(tmem_holder, 512);
@@ -435,28 +448,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 9) {
       if (lane == 0 && n > 0) {
-        const uint64_t pol_kv = policy_evict_first();
-        const uint64_t pol_q = policy_evict_last();
-        mbar_arrive_expect_tx(kv_full, 2 * Cfg::kTileBytes);
-        for (int b = 0; b < Cfg::kBoxes; ++b) {
-          tma_load_4d(sK + b * KA_BOX_BYTES, &tmK, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
-          tma_load_4d(sV + b * KA_BOX_BYTES, &tmV, kv_full, 64 * b, kvh, job.k0, rank, pol_kv);
-        }
         bool ok = true;
-        for (int i = 0; i < n && ok; ++i) {
-          const int st = i % Cfg::kStages;
-          if (!mbar_wait(&empty[st], ((i / Cfg::kStages) & 1) ^ 1, tmo, 131)) {
-            ok = false;
-            break;
-          }
-          const int h = (it0 + i) / nt, x = (it0 + i) - h * nt;
-          mbar_arrive_expect_tx(&raw[st], 2 * Cfg::kQBytes);
-          for (int b = 0; b < Cfg::kBoxes; ++b) {
-            tma_load_4d(sQ + st * Cfg::kQBytes + b * Cfg::kQBox, &tmQ, &raw[st], 64 * b, kvh * prm.group + h,
-                        job.q0 + x * KB2_QT, rank, pol_q);
-            tma_load_4d(sG + st * Cfg::kQBytes + b * Cfg::kQBox, &tmG, &raw[st], 64 * b, kvh * prm.group + h,
-                        job.q0 + x * KB2_QT, rank, pol_q);
-          }
+        for (int i = 1; i < n && ok; ++i) {
+          ok = mbar_wait(&empty[i % Cfg::kStages], ((i / Cfg::kStages) & 1) ^ 1, tmo, 131);
+          if (ok) load_q(i);
         }
         if (!ok) spin_ns(KA_DRAIN_NS);
       }

@@ -9,6 +9,7 @@
 namespace caat {
 
 constexpr int KR_THREADS = 256;
+constexpr int KR_CTAS = 5;         // resident per SM, and launched (10 or 40 measured no faster)
 constexpr int KR_MAX_PAIRS = 128;  // rot <= 256
 
 // Out-of-range device-resident arguments (slots, lengths): reported like the bounded waits' status,
@@ -37,9 +38,10 @@ struct RopeParams {
 // worked out once.  Per token the loads go out first; meanwhile the first rot / 2 threads evaluate the
 // token's angles: in double, since a position times a frequency has to keep its fraction of a turn (at
 // position 10^6 a product rounded to fp32 is off by up to 0.03 rad), reduced to [-1/2, 1/2] turns and
-// then passed on in fp32.  Bound by the memory: T=8192, 32 + 32 heads of 128, 268 MB.
+// then passed on in fp32.  Bound by the memory: T=8192, 32 + 32 heads of 128, 268 MB in 50 us (5.4 TB/s).
+// Two items a thread: 52 us against 57 with four (half of them idle at this size) in the same run.
 template <bool kInterleaved, int kItems>
-__global__ void __launch_bounds__(KR_THREADS, 4) rope_kernel(const __grid_constant__ RopeParams prm) {
+__global__ void __launch_bounds__(KR_THREADS, KR_CTAS) rope_kernel(const __grid_constant__ RopeParams prm) {
   __shared__ float2 cs[2][KR_MAX_PAIRS];
   const int half = prm.rot >> 1;
   const int nrot = kInterleaved ? prm.rot >> 3 : prm.rot >> 4;  // rotated items of a head
