@@ -350,11 +350,12 @@ struct DkvCfg {
   static constexpr int kQBox = KB2_QT * 128;                       // 64 queries x 64 elements
   static constexpr int kQBytes = kBoxes * kQBox;                   // Q or dO: 64 queries
   static constexpr int kStages = HD == 128 ? 4 : 8;
+  static constexpr int kBufs = HD == 128 ? 2 : 3;                  // (S^T | dP^T) in tensor memory beside dV and dK
   static constexpr int kSmem = 1024 + 2 * kTileBytes + kStages * (2 * kQBytes + 2 * KB2_QT * 4) + 512;
 };
 
 // One CTA: 128 keys of one key head, against its share (1 / splits) of the queries of the group's
-// heads, 64 at a time.  Tensor memory: (S^T | dP^T) of even steps | of odd steps | dV | dK, S^T and
+// heads, 64 at a time.  Tensor memory: (S^T | dP^T) of two steps (dh <= 64: three) | dV | dK, S^T and
 // dP^T with the keys in the lanes; p^T and dS^T are written over them and are the A operands of the
 // two sums.  Warps 0-3 take the even steps, 4-7 the odd ones: while one set computes, the tensor
 // cores run the other step's products.  Warp 10 passes on every tile of Q and dO: it zeroes the rows
@@ -379,9 +380,9 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   uint64_t* raw = kv_full + 1;             // [stages] TMA
   uint64_t* full = raw + Cfg::kStages;     // [stages] passed on by warp 10
   uint64_t* empty = full + Cfg::kStages;   // [stages]
-  uint64_t* sd_full = empty + Cfg::kStages;  // [2]
-  uint64_t* pd_full = sd_full + 2;         // [2] 4 warps
-  uint64_t* done = pd_full + 2;
+  uint64_t* sd_full = empty + Cfg::kStages;  // [bufs]
+  uint64_t* pd_full = sd_full + Cfg::kBufs;  // [bufs] 4 warps
+  uint64_t* done = pd_full + Cfg::kBufs;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < Cfg::kBufs; ++b) {
       mbar_init(&sd_full[b], 1);
       mbar_init(&pd_full[b], 4);
     }
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   tc_fence_after();
   constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
   const uint64_t tmo = prm.timeout_ns;
-  constexpr uint32_t kDV = 4 * KB2_QT, kDK = 4 * KB2_QT + HD;
+  constexpr uint32_t kDV = Cfg::kBufs * 2 * KB2_QT, kDK = kDV + HD;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         const uint64_t dQ = sw128_kmajor_desc(smem_u32(sQ)), dG = sw128_kmajor_desc(smem_u32(sG));
         const uint64_t dQt = sw128_mnmajor_desc(smem_u32(sQ)), dGt = sw128_mnmajor_desc(smem_u32(sG));
         int ss = 0, st = 0;  // stages of the next scores and of the next sums
-        uint32_t sp = 0;
+        uint32_t sp = 0, buf = 0, bp = 0;
         auto scores = [&](uint32_t buf) {
           if (!lane_wait(&full[ss], sp, tmo, 132)) return false;
           const uint64_t q = dQ + ss * kQ16, g = dG + ss * kQ16;
@@ -484,10 +485,9 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         };
         bool ok = lane_wait(kv_full, 0, tmo, 133);
 #pragma unroll 1
-        for (int i = -2; i < n && ok; ++i) {
-          const uint32_t buf = i & 1;
+        for (int i = -Cfg::kBufs; i < n && ok; ++i) {
           if (i >= 0) {
-            ok = lane_wait(&pd_full[buf], (i >> 1) & 1, tmo, 134);
+            ok = lane_wait(&pd_full[buf], bp, tmo, 134);
             if (!ok) break;
             tc_fence_after();
             const uint64_t q = dQt + st * kQ16, g = dGt + st * kQ16;
@@ -501,7 +501,11 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
             umma_arrive(lead, &empty[st]);
             if (++st == Cfg::kStages) st = 0;
           }
-          if (i + 2 < n) ok = scores(buf);
+          if (i + Cfg::kBufs < n) ok = scores(buf);
+          if (++buf == Cfg::kBufs) {
+            buf = 0;
+            if (i >= 0) bp ^= 1;
+          }
         }
         umma_arrive(lead, done);
         lane_wait(done, 0, tmo, 135);
@@ -549,12 +553,14 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const uint64_t c2 = pack_f32x2(c, c);
     bool ok = true;
     int x0 = n > 0 ? ((it0 + w) % nt) * KB2_QT : 0;  // the step's first query
+    int buf = w;
+    uint32_t bp = 0;
     for (int i = w; i < n; i += 2) {
       const int st = i % Cfg::kStages;
-      ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 137) && warp_wait(&sd_full[w], (i >> 1) & 1, tmo, 138);
+      ok = warp_wait(&full[st], (i / Cfg::kStages) & 1, tmo, 137) && warp_wait(&sd_full[buf], bp, tmo, 138);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t base = lanes + w * 2 * KB2_QT;
+      const uint32_t base = lanes + buf * 2 * KB2_QT;
       uint32_t s[64], g[64];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -597,7 +603,11 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pd_full[w]);
+      if (lane == 0) mbar_arrive(&pd_full[buf]);
+      if ((buf += 2) >= Cfg::kBufs) {
+        buf -= Cfg::kBufs;
+        bp ^= 1;
+      }
       x0 += 2 * KB2_QT;
       while (x0 >= nt * KB2_QT) x0 -= nt * KB2_QT;  // the next head
     }
