@@ -13,6 +13,7 @@ import os
 from typing import Optional
 
 import numpy as np
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcaat.so")
@@ -177,6 +178,7 @@ class AttnDecodeArgs(ctypes.Structure):
 
 
 _SIZE_MAX = ctypes.c_size_t(-1).value
+_INLINE_QUERIES = 128 * 160  # the forward needs no workspace up to 160 tiles of 128 queries (a sequence may add one)
 _lib = None
 
 
@@ -612,7 +614,6 @@ def caat_rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none
 
 def _current(t, name):
     """Index of the tensor's device, which has to be the current one: the library queues there."""
-    import torch
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -622,7 +623,6 @@ def _current(t, name):
 
 
 def _raw_stream(stream, dev):
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
@@ -719,7 +719,6 @@ def _rope_out(o, x, name, dtype, dev):
 
 
 def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved, backward, mscale, stream, timing):
-    import torch
     first = q if q is not None else k
     if first is None:
         raise ValueError("caat_rope: q and k are both None")
@@ -785,7 +784,6 @@ def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q
 def _attn_tail(q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
     """What the forward's and the backward's arguments share: (device, what must outlive the call,
     addresses of q, k and v, the last fields of the structure)."""
-    import torch
     dev = _current(q, "q")
     bf = torch.bfloat16
     q_ptr, *qs = _heads4(q, "q", bf, dev)
@@ -801,9 +799,11 @@ def _attn_tail(q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
         ck, ck_ptr, nk = _offsets(cu_k, "cu_k")
         if nk != n:
             raise ValueError("cu_q and cu_k must have the same length")
-    need = lib().caat_attn_workspace_size(Tq, Tk, n - 1, P, hq, hk, dh, variant)
-    if need == _SIZE_MAX:
-        need = 0  # sizes the call itself refuses
+    need = 0
+    if workspace is None and (variant != CAAT_VARIANT_ATTN or Tq + 128 * n > _INLINE_QUERIES):
+        need = lib().caat_attn_workspace_size(Tq, Tk, n - 1, P, hq, hk, dh, variant)
+        if need == _SIZE_MAX:
+            need = 0  # sizes the call itself refuses
     ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
     return dev, (cq, ck, ws), (q_ptr, k_ptr, v_ptr), (
         cq_ptr, ck_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev), None if timing is None else timing.handle, Tq, Tk, *qs,
@@ -818,7 +818,6 @@ def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optiona
     cu_q, cu_k: host offsets [n_seq + 1] of the sequences' queries and keys (cu_k None: cu_q; the last
     query sees the last key); out [P,Tq,heads_q*dh] bf16, the X of caat_rowpar_forward; lse
     [P,heads_q,Tq] fp32, needed by the backward.  scale None: dh ** -0.5."""
-    import torch
     dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN, workspace, stream, timing)
     P, Tq, hq, dh = q.shape
     a = AttnArgs(*qkv, _like(out, "out", torch.bfloat16, (P, Tq, hq * dh), dev),
@@ -832,7 +831,6 @@ def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, 
                        workspace=None, stream=None, timing=None):
     """Queues the gradients of caat_attn_forward: dq [P,Tq,heads_q,dh], dk, dv [P,Tk,heads_k,dh] (bf16,
     contiguous) from the forward's inputs, its out and lse, and dout [P,Tq,heads_q*dh]."""
-    import torch
     dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN_BWD, workspace, stream, timing)
     bf = torch.bfloat16
     P, Tq, hq, dh = q.shape
@@ -850,7 +848,6 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
 
     q [P,B,heads_q,dh], caches [P,B,capacity,heads_k,dh] (bf16), lens CUDA int32 [B] (keys of each
     sequence, the new token's included), out [P,B,heads_q*dh]: the X of caat_rowpar_forward."""
-    import torch
     bf = torch.bfloat16
     dev = _current(q, "q")
     q_ptr, *qs = _heads4(q, "q", bf, dev)
