@@ -65,6 +65,43 @@ def test_lengths_outside_the_cache_are_reported():
     assert torch.equal(out[0, 1], decode(q[:, 1:2], kc[:, 1:2], vc[:, 1:2], [10])[0, 0])
 
 
+def test_same_bits_every_time_and_from_a_fused_projection():
+    """The parts of a cut sequence are joined in a fixed order, whichever CTA finishes last; q may be a
+    slice of a fused projection."""
+    P, B, hq, hk, dh, cap = 2, 5, 8, 2, 64, 3000
+    lens = [3000, 1, 777, 2999, 64]
+    qkv = draw(30, P, B, (hq + 2 * hk) * dh).cuda()
+    q = qkv[..., :hq * dh].unflatten(-1, (hq, dh))
+    kc, vc = draw(31, P, B, cap, hk, dh).cuda(), draw(32, P, B, cap, hk, dh).cuda()
+    first = decode(q.contiguous(), kc, vc, lens)
+    for _ in range(10):
+        assert torch.equal(first, decode(q, kc, vc, lens))
+
+
+def test_cache_past_two_to_the_31_elements():
+    """Append to and decode from rows whose element offset does not fit in 32 bits."""
+    B, cap, hk, hq, dh = 16, 140000, 8, 8, 128
+    k = torch.empty(1, B, cap, hk, dh, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    assert k.numel() > 1 << 31
+    n = 300
+    small_k, small_v, q = draw(33, 1, n, hk, dh).cuda(), draw(34, 1, n, hk, dh).cuda(), draw(35, 1, B, hq, dh).cuda()
+    freq, _ = C.caat_rope_frequencies(dh)
+    slots = torch.arange((B - 1) * cap, (B - 1) * cap + n, device="cuda")
+    C.caat_rope_append(None, small_k, small_v, None, slots, freq, k, v)
+    kr = torch.empty_like(small_k)
+    C.caat_rope(small_k, None, None, freq, q_out=kr, k_out=None)
+    assert torch.equal(k[0, -1, :n], kr[0]) and torch.equal(v[0, -1, :n], small_v[0])
+    lens = [0] * (B - 1) + [n]
+    out = decode(q, k, v, lens)
+    assert C.caat_get_device_status() == 0
+    want = decode(q[:, -1:], kr.view(1, 1, n, hk, dh), small_v.view(1, 1, n, hk, dh), [n])
+    ref = A.decode(q[:, -1:].cpu(), kr.view(1, 1, n, hk, dh).cpu(), small_v.view(1, 1, n, hk, dh).cpu(), [n])
+    check_out(out[:, -1:].cpu(), ref)
+    check_out(want.cpu(), ref)
+    assert bool((out[:, :-1] == 0).all())
+
+
 def test_large_scores():
     q, kc, vc = 8 * draw(10, 1, 2, 4, 128), 4 * draw(11, 1, 2, 500, 2, 128), draw(12, 1, 2, 500, 2, 128)
     check_out(decode(q, kc, vc, [500, 300]).cpu(), A.decode(q, kc, vc, [500, 300]))

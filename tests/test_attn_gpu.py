@@ -73,6 +73,10 @@ CASES = [
     (1, 2, 2, 64, [0, 0, 17], None),
     (1, 1, 1, 128, [5], [0]),
     (1, 16, 2, 64, [90, 260], [400, 261]),
+    # more work items than SMs, several to a CTA
+    (8, 4, 4, 128, [300, 1, 129, 260], None),
+    (4, 8, 2, 128, [140, 70, 257, 3, 128], [150, 70, 300, 2, 128]),
+    (64, 1, 1, 16, [65, 64, 63], None),
 ]
 
 
@@ -275,3 +279,77 @@ def test_gradient_against_differences():
         # each of the n elements is off by a few bf16 steps at most, with a sign of its own; u ~ N(0, 1):
         # 6 standard deviations of the sum of n independent errors of 3 u |element|, and the O(h^2) difference
         assert abs((t * u).sum() - slope) <= 6 * 3 * 2.0 ** -8 * np.sqrt((t * t).sum()) + 1e-4 * abs(slope)
+
+
+def test_values_that_are_not_finite_in_many_sequences():
+    """As above with several work items per CTA: each sequence has its own odd token (NaN, +inf, -inf or
+    none), and nothing of it is left for the next."""
+    rng = np.random.default_rng(3)
+    lens = rng.integers(20, 150, 250).tolist()
+    d = make(1, 2, 1, 64, lens, seed=16)
+    out, _ = forward(d)
+    e = {n: (x.clone() if torch.is_tensor(x) else x) for n, x in d.items()}
+    odd = []
+    for i, n in enumerate(lens):
+        at, col, value = int(rng.integers(0, n)), int(rng.integers(0, 64)), [np.nan, np.inf, -np.inf, None][i % 4]
+        odd.append((at, col, value))
+        if value is not None:
+            e["v"][0, d["cu_k"][i] + at, 0, col] = value
+    out2, _ = forward(e)
+    a, b = (x.view(-1, 2, 64).float().cpu().numpy() for x in (out, out2))
+    for i, (at, col, value) in enumerate(odd):
+        q0, q1 = d["cu_q"][i], d["cu_q"][i + 1]
+        want = a[q0:q1].copy()
+        if value is not None:
+            want[at:, :, col] = value
+        np.testing.assert_array_equal(b[q0:q1], want)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with its own workspace, give what they give alone."""
+    many = make(1, 2, 1, 64, [(5 * i) % 31 for i in range(600)], seed=17)
+    long = make(2, 2, 2, 128, [900], seed=18)
+    want = [forward(x) for x in (many, long)]
+    grads = [backward(x, *w) for x, w in zip((many, long), want)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for x, w, st in zip((many, long), want, streams):
+        with torch.cuda.stream(st):
+            t = {n: x[n].cuda() for n in ("q", "k", "v", "dout")}
+            o, l = torch.empty_like(w[0]), torch.empty_like(w[1])
+            g = [torch.empty_like(t[n]) for n in ("q", "k", "v")]
+            for _ in range(5):
+                C.caat_attn_forward(t["q"], t["k"], t["v"], x["cu_q"], o, lse=l)
+                C.caat_attn_backward(t["q"], t["k"], t["v"], o, l, t["dout"], x["cu_q"], *g)
+            got.append((o, l, g, t))
+    torch.cuda.synchronize()
+    assert C.caat_get_device_status() == 0
+    for (o, l, g, _), w, h in zip(got, want, grads):
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+        assert all(torch.equal(x, h[n]) for x, n in zip(g, ("dq", "dk", "dv")))
+
+
+def test_rows_past_two_to_the_31_elements():
+    """Rows whose element offset does not fit in 32 bits: the last tokens of a buffer of 2.2 10^9 elements
+    (those before the only sequence are never touched, and never read)."""
+    hq, hk, dh, n = 16, 1, 128, 200
+    T = (1 << 31) // (hq * dh) + 30000
+    small = make(1, hq, hk, dh, [n], seed=19)
+    want, lse_w = forward(small)
+    q = torch.empty(1, T, hq, dh, dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.empty(1, T, hk, dh, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    out, dout = (torch.empty(1, T, hq * dh, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lse = torch.empty(1, hq, T, dtype=torch.float32, device="cuda")
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (dout, "dout")):
+        t[:, T - n:] = small[name].cuda()
+    cu = [T - n, T]
+    C.caat_attn_forward(q, k, v, cu, out, lse=lse)
+    assert torch.equal(out[:, T - n:], want) and torch.equal(lse[..., T - n:], lse_w)
+    dq, dk, dv = (torch.empty_like(x) for x in (q, k, v))
+    C.caat_attn_backward(q, k, v, out, lse, dout, cu, dq, dk, dv)
+    # a longer buffer's key sums are split differently, so these go against the oracle, not bit for bit
+    M = A.attention(small["q"], small["k"], small["v"], [0, n])["M"]
+    ref = A.attention_backward(small["q"], small["k"], small["v"], want.cpu(), lse_w.cpu(), small["dout"], [0, n])
+    check_grads({"dq": dq[:, T - n:].cpu(), "dk": dk[:, T - n:].cpu(), "dv": dv[:, T - n:].cpu()}, ref, M, dh)
+    assert C.caat_get_device_status() == 0
