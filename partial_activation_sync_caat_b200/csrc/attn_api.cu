@@ -116,6 +116,7 @@ caat_status attn_setup(int* sms) {
   if (!smem(caat::attn_fwd_kernel<64>, caat::FwdCfg<64>::kSmem) || !smem(caat::attn_fwd_kernel<128>, caat::FwdCfg<128>::kSmem) ||
       !smem(caat::attn_dq_kernel<64>, caat::DqCfg<64>::kSmem) || !smem(caat::attn_dq_kernel<128>, caat::DqCfg<128>::kSmem) ||
       !smem(caat::attn_decode_kernel<64>, caat::KD_SMEM) || !smem(caat::attn_decode_kernel<128>, caat::KD_SMEM) ||
+      !smem(caat::attn_decode_cluster_kernel<64>, caat::KD_SMEM) || !smem(caat::attn_decode_cluster_kernel<128>, caat::KD_SMEM) ||
       !smem(caat::attn_dkv_kernel<64>, caat::DkvCfg<64>::kSmem) || !smem(caat::attn_dkv_kernel<128>, caat::DkvCfg<128>::kSmem))
     return CAAT_ERR_CUDA;
   done[dev] = ctx;
@@ -190,6 +191,21 @@ BwdLayout bwd_layout(int64_t Tq, int64_t Tk, int n_seq, int P, int hq, int hk, i
   L.part = L.k_list + list_bytes(max_jobs(Tk, n_seq, caat::KA_TILE));
   L.total = L.part + (L.splits > 1 ? align256(size_t(2) * L.splits * P * Tk * hk * dh * 4) : 0);
   return L;
+}
+
+// CTAs per segment (sequence, rank, key head, 16 query heads) of the decode kernel with a cluster for each, 0
+// for the kernel that deals tiles evenly.  Clusters are as large as it takes for two CTAs per SM and for
+// parts of 2048 keys at most, so that a ragged batch's longest sequence ends with the others.  They start
+// slowly when more of them come than the SMs hold at once, which only parts of 1 MiB make up for (us,
+// clusters | even deal; dh 128: 32 segments of 2048 keys 8.6 | 15.5, of 8192 26.2 | 35.8; 512 of 256 keys
+// with 2 CTAs each 34.2 | 19.0, of 8192 with 4 301 | 331; 2048 of 256 keys, one CTA each, 47.9 | 54.4).
+int decode_cluster(int64_t B, int64_t capacity, int P, int hq, int hk, int dh) {
+  const int64_t segs = B * P * hk * ((hq / hk + 15) / 16);
+  const int tile = 4 * caat::kd_keys(dh <= 64 ? 64 : 128);
+  int c = 1;
+  while (c < 8 && (capacity > 2048 * c || (segs * c < 2 * 148 && 2 * c * tile <= capacity))) c *= 2;
+  if (capacity > 2048 * c || segs * c < 148 || segs * c > INT32_MAX) return 0;
+  return c == 1 || segs * c <= 4 * 148 || capacity / c * dh * 4 >= (1 << 20) ? c : 0;
 }
 
 // The list into the launch's arguments, or through `dst` in the workspace (queued on the stream).
@@ -460,6 +476,7 @@ size_t caat_attn_workspace_size(int64_t Tq, int64_t Tk, int n_seq, int P, int he
     case CAAT_VARIANT_ATTN: return n_seq < 0 ? SIZE_MAX : list_bytes(max_jobs(Tq, n_seq, caat::KA_TILE));
     case CAAT_VARIANT_ATTN_BWD: return n_seq < 0 ? SIZE_MAX : bwd_layout(Tq, Tk, n_seq, P, heads_q, heads_k, dh).total;
     case CAAT_VARIANT_ATTN_DECODE:
+      if (decode_cluster(Tq, Tk, P, heads_q, heads_k, dh) > 0) return 0;
       return kDecodeCounters + align256(size_t(caat::KD_CTAS) * 2 * std::min(heads_q / heads_k, 16) * (dh + 2) * 4);
   }
   return SIZE_MAX;
@@ -570,7 +587,8 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
       meet(out, range_of(a->lens, size_t(a->B) * 4)))
     return CAAT_ERR_INVALID_ARG;
   const size_t need = caat_attn_workspace_size(a->B, a->capacity, 0, a->P, a->heads_q, a->heads_k, a->dh, CAAT_VARIANT_ATTN_DECODE);
-  if (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)) return CAAT_ERR_WORKSPACE;
+  if (need > 0 && (!a->workspace || a->ws_bytes < need || (reinterpret_cast<uintptr_t>(a->workspace) & 255u)))
+    return CAAT_ERR_WORKSPACE;
   int sms = 0;
   if ((s = attn_setup(&sms)) != CAAT_OK) return s;
   caat::DecodeAttnParams p{};
@@ -579,8 +597,6 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   p.v = reinterpret_cast<const __nv_bfloat16*>(a->v_cache);
   p.lens = a->lens;
   p.out = reinterpret_cast<__nv_bfloat16*>(a->out);
-  p.count = static_cast<unsigned int*>(a->workspace);
-  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kDecodeCounters);
   p.q_rank = q.rank;
   p.q_tok = q.tok;
   p.B = a->B;
@@ -596,28 +612,43 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   p.scale = a->scale;
   const int HD = a->dh <= 64 ? 64 : 128;
   const int tile = 4 * caat::kd_keys(HD);
-  const int stage = tile * 2 * HD * 2, index = static_cast<int>(a->B + 5) * 4;
-  const int merge = 4 * p.rows * (HD + 2) * 4;
-  p.stages = std::min(5, (caat::KD_SMEM - merge - index) / stage);
-  const int bytes = p.stages * stage + merge + index;
-  const int64_t most = int64_t(p.G) * a->B * ((a->capacity + tile - 1) / tile);
-  const int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(caat::KD_CTAS, most)));
-  Recorder rec;
-  rec.begin(a->timing, a->stream);
-  caat::attn_decode_clear_kernel<<<1, caat::KD_CTAS, 0, a->stream>>>(p.count);
-  if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+  const int stage = tile * 2 * HD * 2, merge = 4 * p.rows * (HD + 2) * 4;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(caat::KD_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = bytes;
   cfg.stream = a->stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = HD == 64 ? cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<64>, p)
-                                 : cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<128>, p);
+  Recorder rec;
+  rec.begin(a->timing, a->stream);
+  cudaError_t e;
+  const int cluster = decode_cluster(a->B, a->capacity, a->P, a->heads_q, a->heads_k, a->dh);
+  if (cluster > 0) {
+    const int own = p.rows * 2 * 4;  // the CTA's maxima and sums
+    p.stages = std::min(5, (caat::KD_SMEM - merge - own) / stage);
+    cfg.gridDim = dim3(static_cast<unsigned>(a->B * p.G * cluster), 1, 1);
+    cfg.dynamicSmemBytes = p.stages * stage + merge + own;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    e = HD == 64 ? cudaLaunchKernelEx(&cfg, caat::attn_decode_cluster_kernel<64>, p, cluster)
+                 : cudaLaunchKernelEx(&cfg, caat::attn_decode_cluster_kernel<128>, p, cluster);
+  } else {
+    p.count = static_cast<unsigned int*>(a->workspace);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + kDecodeCounters);
+    const int index = static_cast<int>(a->B + 5) * 4;
+    p.stages = std::min(5, (caat::KD_SMEM - merge - index) / stage);
+    const int64_t most = int64_t(p.G) * a->B * ((a->capacity + tile - 1) / tile);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(caat::KD_CTAS, most))), 1, 1);
+    cfg.dynamicSmemBytes = p.stages * stage + merge + index;
+    caat::attn_decode_clear_kernel<<<1, caat::KD_CTAS, 0, a->stream>>>(p.count);
+    if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    e = HD == 64 ? cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<64>, p)
+                 : cudaLaunchKernelEx(&cfg, caat::attn_decode_kernel<128>, p);
+  }
   if (e != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
   return CAAT_OK;

@@ -127,6 +127,12 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint3
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Two floats of another CTA's shared memory (a shared::cluster address).
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -185,6 +191,165 @@ __device__ __noinline__ void decode_join(const DecodeAttnParams& prm, int z0, in
   }
 }
 
+// A warp's share of a segment: the query rows as MMA fragments, the running maximum and sum of the
+// thread's two rows (r0, r0 + 8) and the sums of p v.
+template <int HD>
+struct DecodeWarp {
+  static constexpr int kKeys = kd_keys(HD);
+  static constexpr int kRow = HD * 2;  // bytes of a key's row in shared memory
+  uint32_t qa[HD / 16][4];
+  float o[HD / 8][4];
+  float m[2], l[2];
+  int lane, r0;
+
+  __device__ __forceinline__ void begin(const __nv_bfloat16* q, int rows, int dh) {
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = r0 + 8 * (e & 1), d = 16 * kk + 8 * (e >> 1) + 2 * (lane & 3);
+        qa[kk][e] = (r < rows && d < dh) ? *reinterpret_cast<const uint32_t*>(q + r * dh + d) : 0u;
+      }
+#pragma unroll
+    for (int x = 0; x < HD / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+
+  // The warp's keys of a tile, `live` of them before the sequence's end; K rows at ks, V rows at vs.
+  __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, int live, float c) {
+    float s[kKeys / 8][4] = {};
+    const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;  // ldmatrix row and chunk of the lane
+#pragma unroll
+    for (int kk = 0; kk < HD / 16; ++kk)
+#pragma unroll
+      for (int x = 0; x < kKeys / 16; ++x) {
+        uint32_t b[4];
+        ldmatrix_x4(ks + (16 * x + kr) * kRow + (((2 * kk + kc) ^ (kr & 7)) << 4), b);
+        mma_16816(s[2 * x], qa[kk], b[0], b[1]);
+        mma_16816(s[2 * x + 1], qa[kk], b[2], b[3]);
+      }
+    float top[2] = {m[0], m[1]};
+#pragma unroll
+    for (int x = 0; x < kKeys / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[x][e] *= c;
+        if (live < kKeys) {
+          const int key = 8 * x + 2 * (lane & 3) + (e & 1);
+          s[x][e] = key < live ? s[x][e] : -INFINITY;
+        }
+        top[e >> 1] = fmaxf(top[e >> 1], s[x][e]);
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
+    }
+    // the maximum only moves when exceeded by 2^8: p stays below 256, the quotient is the same
+    if (__any_sync(0xFFFFFFFFu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = top[e] > m[e] ? ex2(m[e] - top[e]) : 1.f;
+        m[e] = top[e];
+        l[e] *= f;
+#pragma unroll
+        for (int x = 0; x < HD / 8; ++x) {
+          o[x][2 * e] *= f;
+          o[x][2 * e + 1] *= f;
+        }
+      }
+    }
+    uint32_t pa[kKeys / 16][4];
+#pragma unroll
+    for (int x = 0; x < kKeys / 8; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float base = m[e] == -INFINITY ? 0.f : m[e];
+        const float p0 = ex2(s[x][2 * e] - base), p1 = ex2(s[x][2 * e + 1] - base);
+        l[e] += p0 + p1;
+        pa[x >> 1][2 * (x & 1) + e] = pack_bf16x2(p0, p1);
+      }
+    const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
+#pragma unroll
+    for (int y = 0; y < kKeys / 16; ++y)
+#pragma unroll
+      for (int x = 0; x < HD / 16; ++x) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(vs + (16 * y + vr) * kRow + (((2 * x + vc) ^ (vr & 7)) << 4), b);
+        mma_16816(o[2 * x], pa[y], b[0], b[1]);
+        mma_16816(o[2 * x + 1], pa[y], b[2], b[3]);
+      }
+  }
+
+  // This warp's results into merge [4][all_rows][HD] and ml [4][all_rows][2].
+  __device__ __forceinline__ void publish(float* merge, float* ml, int warp, int rows, int all_rows) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+      l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+      const int r = r0 + 8 * e;
+      if (r < rows) {
+        float* row = merge + (warp * all_rows + r) * HD;
+#pragma unroll
+        for (int x = 0; x < HD / 8; ++x)
+          *reinterpret_cast<float2*>(row + 8 * x + 2 * (lane & 3)) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
+        if ((lane & 3) == 0) {
+          ml[(warp * all_rows + r) * 2] = m[e];
+          ml[(warp * all_rows + r) * 2 + 1] = l[e];
+        }
+      }
+    }
+  }
+};
+
+// The four warps' results of elements d, d + 1 of row r: maximum, sum, sums of p v.
+template <int HD>
+__device__ __forceinline__ void decode_merge(const float* merge, const float* ml, int all_rows, int r, int d, float& M, float& L,
+                                             float& x0, float& x1) {
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[(w * all_rows + r) * 2]);
+  const float base = M == -INFINITY ? 0.f : M;
+  L = x0 = x1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ex2(ml[(w * all_rows + r) * 2] - base);
+    const float2 x = *reinterpret_cast<const float2*>(merge + (w * all_rows + r) * HD + d);
+    L = fmaf(f, ml[(w * all_rows + r) * 2 + 1], L);
+    x0 = fmaf(f, x.x, x0);
+    x1 = fmaf(f, x.y, x1);
+  }
+}
+
+__device__ __forceinline__ void cp_async_wait_stages(int stages) {  // all but the stages - 1 newest groups
+  switch (stages) {
+    case 2: cp_async_wait<1>(); break;
+    case 3: cp_async_wait<2>(); break;
+    case 4: cp_async_wait<3>(); break;
+    default: cp_async_wait<4>(); break;
+  }
+}
+
+// A lane's copies of a tile: one 16-byte piece of every kStep-th of the warp's keys.  `ahead`: keys left
+// from the lane's first one on (0 where its piece lies past dh).
+template <int HD>
+__device__ __forceinline__ void decode_copy(uint32_t dst, const __nv_bfloat16* kp, const __nv_bfloat16* vp, int64_t tok, int ahead,
+                                            const __nv_bfloat16* any, int lane) {
+  constexpr int kKeys = kd_keys(HD), kRow = HD * 2, kChunks = HD / 8, kStep = 32 / kChunks;
+  const int chunk = lane % kChunks;
+#pragma unroll
+  for (int i = 0; i < kKeys / kStep; ++i) {
+    const int r = i * kStep + lane / kChunks;
+    const bool in = i * kStep < ahead;
+    const uint32_t d = dst + r * kRow + ((chunk ^ (r & 7)) << 4);
+    cp_async_16(d, in ? kp + i * kStep * tok : any, in ? 16 : 0);
+    cp_async_16(d + kKeys * kRow, in ? vp + i * kStep * tok : any, in ? 16 : 0);
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid_constant__ DecodeAttnParams prm) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -193,7 +358,6 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
   constexpr int kRow = HD * 2;                 // bytes of a key's row in shared memory
   constexpr int kStage = 2 * kKeys * kRow;     // a warp's keys of K and of V
   constexpr int kChunks = HD / 8;
-  constexpr int kStep = 32 / kChunks;          // keys that one copy instruction of the warp covers
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem_raw + warp * prm.stages * kStage;
   float* merge = reinterpret_cast<float*>(smem_raw + 4 * prm.stages * kStage);  // [4][rows][HD]
@@ -251,14 +415,7 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
         fresh_ld = false;
       }
       const uint32_t dst = smem_u32(ring + stage * kStage);
-#pragma unroll
-      for (int i = 0; i < kKeys / kStep; ++i) {
-        const int r = i * kStep + lane / kChunks;
-        const bool in = i * kStep < ahead;
-        const uint32_t d = dst + r * kRow + ((my_chunk ^ (r & 7)) << 4);
-        cp_async_16(d, in ? kp + i * kStep * tok : prm.k, in ? 16 : 0);
-        cp_async_16(d + kKeys * kRow, in ? vp + i * kStep * tok : prm.v, in ? 16 : 0);
-      }
+      decode_copy<HD>(dst, kp, vp, tok, ahead, prm.k, lane);
       kp += kTile * tok;
       vp += kTile * tok;
       ahead -= kTile;
@@ -271,10 +428,9 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
 
   for (int s = 0; s < prm.stages - 1; ++s) load(s);
   const float c = prm.scale * KA_LOG2E;
-  const int r0 = lane >> 2;  // the thread's rows: r0, r0 + 8
-  uint32_t qa[HD / 16][4];
-  float o[HD / 8][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  DecodeWarp<HD> w;
+  w.lane = lane;
+  w.r0 = lane >> 2;
   int rank = 0, kvh = 0, gb = 0, rows = 0, head0 = 0, len = 0;
   bool fresh = true;
   int stage = 0, ld_stage = prm.stages - 1;
@@ -284,119 +440,23 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       rows = min(prm.group - 16 * gb, 16);
       head0 = kvh * prm.group + 16 * gb;
       len = __ldg(prm.lens + at.b);
-      const __nv_bfloat16* q = prm.q + rank * prm.q_rank + at.b * prm.q_tok + int64_t(head0) * prm.dh;
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 8 * (e & 1), d = 16 * kk + 8 * (e >> 1) + 2 * (lane & 3);
-          qa[kk][e] = (r < rows && d < prm.dh) ? *reinterpret_cast<const uint32_t*>(q + r * prm.dh + d) : 0u;
-        }
-#pragma unroll
-      for (int x = 0; x < HD / 8; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[x][e] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+      w.begin(prm.q + rank * prm.q_rank + at.b * prm.q_tok + int64_t(head0) * prm.dh, rows, prm.dh);
       fresh = false;
     }
     load(ld_stage);
     ld_stage = ld_stage + 1 == prm.stages ? 0 : ld_stage + 1;
-    switch (prm.stages) {
-      case 2: cp_async_wait<1>(); break;
-      case 3: cp_async_wait<2>(); break;
-      case 4: cp_async_wait<3>(); break;
-      default: cp_async_wait<4>(); break;
-    }
+    cp_async_wait_stages(prm.stages);
     __syncwarp();
     const uint32_t ks = smem_u32(ring + stage * kStage), vs = ks + kKeys * kRow;
     const int live = len - (at.t * kTile + warp * kKeys);
-    if (live > 0) {
-      float s[kKeys / 8][4] = {};
-      const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;  // ldmatrix row and chunk of the lane
-#pragma unroll
-      for (int kk = 0; kk < HD / 16; ++kk)
-#pragma unroll
-        for (int x = 0; x < kKeys / 16; ++x) {
-          uint32_t b[4];
-          ldmatrix_x4(ks + (16 * x + kr) * kRow + (((2 * kk + kc) ^ (kr & 7)) << 4), b);
-          mma_16816(s[2 * x], qa[kk], b[0], b[1]);
-          mma_16816(s[2 * x + 1], qa[kk], b[2], b[3]);
-        }
-      float top[2] = {m[0], m[1]};
-#pragma unroll
-      for (int x = 0; x < kKeys / 8; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[x][e] *= c;
-          if (live < kKeys) {
-            const int key = 8 * x + 2 * (lane & 3) + (e & 1);
-            s[x][e] = key < live ? s[x][e] : -INFINITY;
-          }
-          top[e >> 1] = fmaxf(top[e >> 1], s[x][e]);
-        }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 1));
-        top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], 2));
-      }
-      // the maximum only moves when exceeded by 2^8: p stays below 256, the quotient is the same
-      if (__any_sync(0xFFFFFFFFu, top[0] - m[0] > 8.f || top[1] - m[1] > 8.f)) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float f = top[e] > m[e] ? ex2(m[e] - top[e]) : 1.f;
-          m[e] = top[e];
-          l[e] *= f;
-#pragma unroll
-          for (int x = 0; x < HD / 8; ++x) {
-            o[x][2 * e] *= f;
-            o[x][2 * e + 1] *= f;
-          }
-        }
-      }
-      uint32_t pa[kKeys / 16][4];
-#pragma unroll
-      for (int x = 0; x < kKeys / 8; ++x)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float base = m[e] == -INFINITY ? 0.f : m[e];
-          const float p0 = ex2(s[x][2 * e] - base), p1 = ex2(s[x][2 * e + 1] - base);
-          l[e] += p0 + p1;
-          pa[x >> 1][2 * (x & 1) + e] = pack_bf16x2(p0, p1);
-        }
-      const int vr = (lane & 7) + (((lane >> 3) & 1) << 3), vc = lane >> 4;
-#pragma unroll
-      for (int y = 0; y < kKeys / 16; ++y)
-#pragma unroll
-        for (int x = 0; x < HD / 16; ++x) {
-          uint32_t b[4];
-          ldmatrix_x4_trans(vs + (16 * y + vr) * kRow + (((2 * x + vc) ^ (vr & 7)) << 4), b);
-          mma_16816(o[2 * x], pa[y], b[0], b[1]);
-          mma_16816(o[2 * x + 1], pa[y], b[2], b[3]);
-        }
-    }
+    if (live > 0) w.tile(ks, vs, live, c);
     __syncwarp();
     stage = stage + 1 == prm.stages ? 0 : stage + 1;
 
     const bool ends = at.t + 1 == at.tiles;
     if (ends || left == 1) {
       // the CTA's part of the segment: merge the four warps
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-        const int r = r0 + 8 * e;
-        if (r < rows) {
-          float* row = merge + (warp * prm.rows + r) * HD;
-#pragma unroll
-          for (int x = 0; x < HD / 8; ++x)
-            *reinterpret_cast<float2*>(row + 8 * x + 2 * (lane & 3)) = make_float2(o[x][2 * e], o[x][2 * e + 1]);
-          if ((lane & 3) == 0) {
-            ml[(warp * prm.rows + r) * 2] = m[e];
-            ml[(warp * prm.rows + r) * 2 + 1] = l[e];
-          }
-        }
-      }
+      w.publish(merge, ml, warp, rows, prm.rows);
       __syncthreads();
       const bool starts_here = left + at.t <= i1 - i0;  // the segment's first tile is this CTA's
       const bool complete = ends && starts_here;
@@ -404,19 +464,8 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       for (int i = threadIdx.x; i < rows * (HD / 2); i += KD_THREADS) {
         const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
         if (d >= prm.dh) continue;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, ml[(w * prm.rows + r) * 2]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f, x0 = 0.f, x1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float f = ex2(ml[(w * prm.rows + r) * 2] - base);
-          const float2 x = *reinterpret_cast<const float2*>(merge + (w * prm.rows + r) * HD + d);
-          L = fmaf(f, ml[(w * prm.rows + r) * 2 + 1], L);
-          x0 = fmaf(f, x.x, x0);
-          x1 = fmaf(f, x.y, x1);
-        }
+        float M, L, x0, x1;
+        decode_merge<HD>(merge, ml, prm.rows, r, d, M, L, x0, x1);
         if (complete) {
           const float inv = 1.f / L;
           *reinterpret_cast<uint32_t*>(prm.out + ((rank * prm.B + at.b) * prm.hq + head0 + r) * prm.dh + d) =
@@ -445,6 +494,125 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
     at.next(prm, pre);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (every block, so that the clearing never outlives this kernel)
+}
+
+// The same with a cluster of CTAs per segment instead of the even deal: each CTA takes an equal part of the
+// segment's tiles, and the parts are joined through distributed shared memory, so that there is one
+// launch and no workspace.  The deal is kept for what this does badly: fewer segments than fill the
+// SMs 8 CTAs apiece, and contexts so long that one sequence's part would outlast all others.
+template <int HD>
+__global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_cluster_kernel(const __grid_constant__ DecodeAttnParams prm, int ctas) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int kKeys = kd_keys(HD);
+  constexpr int kTile = 4 * kKeys;
+  constexpr int kRow = HD * 2;
+  constexpr int kStage = 2 * kKeys * kRow;
+  constexpr int kChunks = HD / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem_raw + warp * prm.stages * kStage;
+  float* merge = reinterpret_cast<float*>(smem_raw + 4 * prm.stages * kStage);  // [4][rows][HD]
+  float* ml = merge + 4 * prm.rows * HD;                                        // [4][rows][2], then this CTA's [rows][2]
+  const int part = blockIdx.x % ctas;
+  const int64_t seg = blockIdx.x / ctas;
+  // a sequence's segments are neighbours: (sequence, rank, key head, block of heads)
+  const int64_t b = seg / prm.G;
+  const int g = static_cast<int>(seg - b * prm.G);
+  const int gb = g % prm.n_gb, x = g / prm.n_gb, rank = x / prm.hk, kvh = x - rank * prm.hk;
+  const int rows = min(prm.group - 16 * gb, 16), head0 = kvh * prm.group + 16 * gb;
+  const int asked = __ldg(prm.lens + b);
+  const int len = asked > 0 && asked <= prm.capacity ? asked : 0;
+  __nv_bfloat16* out = prm.out + ((rank * prm.B + b) * prm.hq + head0) * prm.dh;
+  if (len == 0) {  // (the whole cluster)
+    if (asked != 0 && g == 0 && threadIdx.x == 0 && part == 0) atomicCAS(&g_arg_status, 0, (82 << 8) | 1);
+    if (part == 0)
+      for (int i = threadIdx.x; i < rows * prm.dh / 8; i += KD_THREADS) st_v4(out + 8 * i, make_uint4(0, 0, 0, 0));
+    return;
+  }
+  const int tiles = (len + kTile - 1) / kTile;
+  const int t0 = static_cast<int>(int64_t(tiles) * part / ctas), t1 = static_cast<int>(int64_t(tiles) * (part + 1) / ctas);
+
+  const int my_key = warp * kKeys + lane / kChunks, my_chunk = lane % kChunks;
+  const int64_t tok = int64_t(prm.hk) * prm.dh;
+  const int64_t off = ((rank * prm.B + b) * prm.capacity + t0 * kTile + my_key) * tok + int64_t(kvh) * prm.dh + my_chunk * 8;
+  const __nv_bfloat16 *kp = prm.k + off, *vp = prm.v + off;
+  int ahead = my_chunk * 8 < prm.dh ? len - t0 * kTile - my_key : 0;
+  int todo = t1 - t0;
+  auto load = [&](int stage) {
+    if (todo > 0) {
+      decode_copy<HD>(smem_u32(ring + stage * kStage), kp, vp, tok, ahead, prm.k, lane);
+      kp += kTile * tok;
+      vp += kTile * tok;
+      ahead -= kTile;
+      --todo;
+    }
+    cp_async_commit();
+  };
+  for (int s = 0; s < prm.stages - 1; ++s) load(s);
+  const float c = prm.scale * KA_LOG2E;
+  DecodeWarp<HD> w;
+  w.lane = lane;
+  w.r0 = lane >> 2;
+  w.begin(prm.q + rank * prm.q_rank + b * prm.q_tok + int64_t(head0) * prm.dh, rows, prm.dh);
+  int stage = 0, ld_stage = prm.stages - 1;
+  for (int t = t0; t < t1; ++t) {
+    load(ld_stage);
+    ld_stage = ld_stage + 1 == prm.stages ? 0 : ld_stage + 1;
+    cp_async_wait_stages(prm.stages);
+    __syncwarp();
+    const uint32_t ks = smem_u32(ring + stage * kStage);
+    const int live = len - (t * kTile + warp * kKeys);
+    if (live > 0) w.tile(ks, ks + kKeys * kRow, live, c);
+    __syncwarp();
+    stage = stage + 1 == prm.stages ? 0 : stage + 1;
+  }
+  w.publish(merge, ml, warp, rows, prm.rows);
+  __syncthreads();
+  float* cta_ml = ml + 4 * prm.rows * 2;
+  for (int i = threadIdx.x; i < rows * (HD / 2); i += KD_THREADS) {
+    const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
+    float M, L, x0, x1;
+    decode_merge<HD>(merge, ml, prm.rows, r, d, M, L, x0, x1);
+    if (ctas == 1) {
+      const float inv = 1.f / L;
+      if (d < prm.dh) *reinterpret_cast<uint32_t*>(out + r * prm.dh + d) = pack_bf16x2(x0 * inv, x1 * inv);
+    } else {
+      *reinterpret_cast<float2*>(merge + r * HD + d) = make_float2(x0, x1);  // over warp 0's, read by this thread alone
+      if (d == 0) {
+        cta_ml[2 * r] = M;
+        cta_ml[2 * r + 1] = L;
+      }
+    }
+  }
+  if (ctas == 1) return;
+  cluster_sync();
+  for (int i = part * KD_THREADS + threadIdx.x; i < rows * (HD / 2); i += ctas * KD_THREADS) {
+    const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
+    if (d >= prm.dh) continue;
+    const uint32_t at_ml = smem_u32(cta_ml + 2 * r), at_x = smem_u32(merge + r * HD + d);
+    float2 pm[8], px[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (z < ctas) {
+        pm[z] = ld_cluster_f32x2(mapa_shared(at_ml, z));
+        px[z] = ld_cluster_f32x2(mapa_shared(at_x, z));
+      }
+    float M = -INFINITY, L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (z < ctas) M = fmaxf(M, pm[z].x);
+    const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (z < ctas) {
+        const float f = ex2(pm[z].x - base);
+        L = fmaf(f, pm[z].y, L);
+        x0 = fmaf(f, px[z].x, x0);
+        x1 = fmaf(f, px[z].y, x1);
+      }
+    const float inv = 1.f / L;
+    *reinterpret_cast<uint32_t*>(out + r * prm.dh + d) = pack_bf16x2(x0 * inv, x1 * inv);
+  }
+  cluster_sync();  // nobody leaves while its results are read
 }
 
 }  // namespace caat

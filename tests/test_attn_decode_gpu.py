@@ -36,7 +36,10 @@ def decode(q, kc, vc, lens, **kw):
     (1, 8, 1, 64, 1000, [1000, 64, 63, 129]), (1, 6, 2, 96, 130, [130, 3]), (1, 2, 2, 8, 77, [77, 50]),
     (1, 16, 1, 128, 200, [199, 17]), (1, 20, 1, 64, 150, [150, 2]), (1, 48, 2, 72, 90, [88, 1, 90]),
     (8, 4, 4, 128, 2000, [1999]), (1, 2, 1, 128, 9000, [8193, 9000]), (1, 3, 1, 120, 70, [0, 0, 70]),
-    (4, 8, 1, 64, 40, [1 + (7 * i) % 40 for i in range(70)])])
+    (4, 8, 1, 64, 40, [1 + (7 * i) % 40 for i in range(70)]),
+    # clusters of 8, 4, 2 and 1 CTAs per segment, of narrow and wide heads, more than 16 query heads to a key head
+    (8, 4, 4, 64, 1500, [0, 1, 1500, 127, 129]), (8, 48, 2, 72, 700, [700, 1, 0, 350, 128, 64]),
+    (16, 2, 2, 128, 130, [130, 64, 65, 1, 0, 129]), (16, 17, 1, 128, 60, [60, 0, 1, 33] * 4), (19, 1, 1, 128, 1024, [1024])])
 def test_matches_oracle(P, hq, hk, dh, cap, lens):
     B = len(lens)
     q, kc, vc = draw(1, P, B, hq, dh), draw(2, P, B, cap, hk, dh), draw(3, P, B, cap, hk, dh)
@@ -45,10 +48,11 @@ def test_matches_oracle(P, hq, hk, dh, cap, lens):
     check_out(out.cpu(), A.decode(q, kc, vc, lens))
 
 
+@pytest.mark.parametrize("P", [1, 20])
 @pytest.mark.parametrize("junk", [float("nan"), float("inf")])
-def test_rows_behind_a_length_are_never_used(junk):
+def test_rows_behind_a_length_are_never_used(junk, P):
     lens = [70, 5, 128, 0]
-    q, kc, vc = draw(4, 1, 4, 4, 64), draw(5, 1, 4, 140, 2, 64), draw(6, 1, 4, 140, 2, 64)
+    q, kc, vc = draw(4, P, 4, 4, 64), draw(5, P, 4, 140, 2, 64), draw(6, P, 4, 140, 2, 64)
     a = decode(q, kc, vc, lens)
     for b, n in enumerate(lens):
         kc[:, b, n:] = junk
@@ -56,19 +60,21 @@ def test_rows_behind_a_length_are_never_used(junk):
     assert torch.equal(a, decode(q, kc, vc, lens))
 
 
-def test_lengths_outside_the_cache_are_reported():
-    q, kc, vc = draw(7, 1, 3, 2, 64), draw(8, 1, 3, 10, 1, 64), draw(9, 1, 3, 10, 1, 64)
+@pytest.mark.parametrize("P", [1, 60])
+def test_lengths_outside_the_cache_are_reported(P):
+    q, kc, vc = draw(7, P, 3, 2, 64), draw(8, P, 3, 10, 1, 64), draw(9, P, 3, 10, 1, 64)
     out = decode(q, kc, vc, [11, 10, -1])
     assert C.caat_get_device_status() & 0xFF == C.CAAT_ERR_INVALID_ARG
     assert C.caat_get_device_status() == 0
-    assert bool((out[0, [0, 2]] == 0).all())
-    assert torch.equal(out[0, 1], decode(q[:, 1:2], kc[:, 1:2], vc[:, 1:2], [10])[0, 0])
+    assert bool((out[:, [0, 2]] == 0).all())
+    check_out(out[:, 1:2].cpu(), A.decode(q[:, 1:2], kc[:, 1:2], vc[:, 1:2], [10]))
 
 
-def test_same_bits_every_time_and_from_a_fused_projection():
+@pytest.mark.parametrize("P", [2, 16])
+def test_same_bits_every_time_and_from_a_fused_projection(P):
     """The parts of a cut sequence are joined in a fixed order, whichever CTA finishes last; q may be a
     slice of a fused projection."""
-    P, B, hq, hk, dh, cap = 2, 5, 8, 2, 64, 3000
+    B, hq, hk, dh, cap = 5, 8, 2, 64, 3000
     lens = [3000, 1, 777, 2999, 64]
     qkv = draw(30, P, B, (hq + 2 * hk) * dh).cuda()
     q = qkv[..., :hq * dh].unflatten(-1, (hq, dh))
@@ -107,10 +113,10 @@ def test_large_scores():
     check_out(decode(q, kc, vc, [500, 300]).cpu(), A.decode(q, kc, vc, [500, 300]))
 
 
-def test_captured_step_follows_the_lengths():
-    """A captured step (append, decode) replayed over a growing context equals separate calls; two
-    graphs with a workspace each."""
-    P, B, hq, hk, dh, cap = 2, 3, 4, 2, 64, 200
+@pytest.mark.parametrize("P", [2, 30])
+def test_captured_step_follows_the_lengths(P):
+    """A captured step (append, decode) replayed over a growing context equals separate calls."""
+    B, hq, hk, dh, cap = 3, 4, 2, 64, 200
     freq, _ = C.caat_rope_frequencies(dh)
     kc, vc = draw(13, P, B, cap, hk, dh).cuda(), draw(14, P, B, cap, hk, dh).cuda()
     kc2, vc2 = kc.clone(), vc.clone()
@@ -118,7 +124,9 @@ def test_captured_step_follows_the_lengths():
     lens = torch.tensor([60, 1, 130], dtype=torch.int32, device="cuda")
     pos, slots, base = lens - 1, (lens - 1).long() + cap * torch.arange(B, device="cuda"), None
     out, qr = torch.empty(P, B, hq * dh, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)
-    ws = C.alloc_workspace(C.caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, C.CAAT_VARIANT_ATTN_DECODE))
+    need = C.caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, C.CAAT_VARIANT_ATTN_DECODE)
+    assert (need == 0) == (P == 30)  # both kernels
+    ws = C.alloc_workspace(need)
 
     def step(kc, vc, out):
         C.caat_rope_append(q, k, v, pos, slots, freq, kc, vc, q_out=qr)
