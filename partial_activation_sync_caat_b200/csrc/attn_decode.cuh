@@ -170,17 +170,25 @@ __device__ __noinline__ void decode_join(const DecodeAttnParams& prm, int z0, in
       if (z + lane <= z1) ml = __ldcg(reinterpret_cast<const float2*>(part(z + lane) + prm.dh));
       const float f = ex2(ml.x - base), fl = f * ml.y;
       const int n = min(32, z1 + 1 - z);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float fi = __shfl_sync(0xFFFFFFFFu, f, i);
-        L += __shfl_sync(0xFFFFFFFFu, fl, i);
+      for (int i0 = 0; i0 < n; i0 += 8) {  // 8 parts' loads at once
+        float2 v[8][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (2 * lane + 64 * e < prm.dh) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(part(z + i) + 2 * lane + 64 * e));
-            o[2 * e] = fmaf(fi, v.x, o[2 * e]);
-            o[2 * e + 1] = fmaf(fi, v.y, o[2 * e + 1]);
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            v[i][e] = i0 + i < n && 2 * lane + 64 * e < prm.dh
+                          ? __ldcg(reinterpret_cast<const float2*>(part(z + i0 + i) + 2 * lane + 64 * e))
+                          : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float fi = __shfl_sync(0xFFFFFFFFu, f, i0 + i);
+          L += __shfl_sync(0xFFFFFFFFu, fl, i0 + i);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[2 * e] = fmaf(fi, v[i][e].x, o[2 * e]);
+            o[2 * e + 1] = fmaf(fi, v[i][e].y, o[2 * e + 1]);
           }
+        }
       }
     }
     const float inv = 1.f / L;
@@ -376,7 +384,14 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
       for (int i = threadIdx.x; i < n; i += KD_THREADS)
         st_v4(prm.out + (r * prm.B + b) * prm.hq * prm.dh + 8 * i, make_uint4(0, 0, 0, 0));
   }
-  const DecodeDeal deal(int64_t(pre[prm.B]) * prm.G, gridDim.x);
+  // (two tiles a CTA at least: parts cost time to join)
+  const int64_t total = int64_t(pre[prm.B]) * prm.G;
+  const int active = static_cast<int>(min(int64_t(gridDim.x), (total + 1) / 2));
+  if (static_cast<int>(blockIdx.x) >= active) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const DecodeDeal deal(total, active);
   const int64_t i0 = deal.begin(blockIdx.x), i1 = deal.begin(blockIdx.x + 1);
   if (i0 == i1) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
