@@ -10,6 +10,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -177,8 +178,16 @@ class AttnDecodeArgs(ctypes.Structure):
     ]
 
 
+# The attention block's calls are short enough for the marshalling to show: their arguments are packed
+# in one go (native layout, the same as the structures above) and passed as bytes.
+_PACK_ROPE = struct.Struct("@11P8q5ifI0P")
+_PACK_ATTN = struct.Struct("@5P2PPN2P8q5ifI0P")
+_PACK_ATTN_BWD = struct.Struct("@9P2PPN2P8q5ifI0P")
+_PACK_ATTN_DECODE = struct.Struct("@6PN2P4q4ifI0P")
+_PACKED = {"caat_rope": (_PACK_ROPE, RopeArgs), "caat_attn_forward": (_PACK_ATTN, AttnArgs),
+           "caat_attn_backward": (_PACK_ATTN_BWD, AttnBwdArgs), "caat_attn_decode": (_PACK_ATTN_DECODE, AttnDecodeArgs)}
+
 _SIZE_MAX = ctypes.c_size_t(-1).value
-_INLINE_QUERIES = 128 * 160  # the forward needs no workspace up to 160 tiles of 128 queries (a sequence may add one)
 _lib = None
 
 
@@ -230,6 +239,11 @@ def lib() -> ctypes.CDLL:
                        ("caat_attn_decode", AttnDecodeArgs)):
         getattr(L, name).argtypes = [ctypes.POINTER(args)]
         getattr(L, name).restype = ctypes.c_int
+    for name, (packed, args) in _PACKED.items():
+        assert packed.size == ctypes.sizeof(args), name
+        fast = L[name]  # a function object of its own
+        fast.argtypes, fast.restype = [ctypes.c_char_p], ctypes.c_int
+        setattr(L, "packed_" + name, fast)
     L.caat_attn_workspace_size.argtypes = [i64, i64] + [ctypes.c_int] * 6
     L.caat_attn_workspace_size.restype = sz
     L.caat_permute_weights.restype = ctypes.c_int
@@ -630,34 +644,39 @@ def _raw_stream(stream, dev):
     return stream.cuda_stream
 
 
-def _like(t, name, dtype, shape, dev, contiguous=True):
-    """Address of a tensor after checks of its type, shape, device and layout."""
+def _like(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor after checks of its type, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _refuse(t, name, dtype, shape, dev):
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 def _heads4(t, name, dtype, dev, shape=None):
     """Address and (rank, token) strides of a [P, T, heads, dh] tensor whose heads lie side by side
-    within a token (a contiguous tensor, or a slice of a fused projection)."""
+    within a token (a contiguous tensor, strides 0, or a slice of a fused projection)."""
     if t.dim() != 4:
         raise ValueError(f"{name} must be [P, T, heads, dh]")
-    ptr = _like(t, name, dtype, t.shape if shape is None else shape, dev, contiguous=False)
-    P, T, heads, dh = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or (shape is not None and t.shape != shape):
+        _refuse(t, name, dtype, t.shape if shape is None else shape, dev)
     if t.is_contiguous():
-        return ptr, T * heads * dh, heads * dh
+        return t.data_ptr(), 0, 0
+    P, T, heads, dh = t.shape
     s = t.stride()
     if (dh > 1 and s[3] != 1) or (heads > 1 and s[2] != dh):
         raise ValueError(f"{name}: the heads of a token must be contiguous and side by side")
     # a dimension of one element has no stride of its own
     token = s[1] if T > 1 else heads * dh
-    return ptr, s[0] if P > 1 else max(s[0], token * T), token
+    return t.data_ptr(), s[0] if P > 1 else max(s[0], token * T), token
 
 
 def _workspace(workspace, nbytes, dev, stream):
@@ -712,9 +731,9 @@ def _rope_out(o, x, name, dtype, dev):
     if o is x:
         return x.data_ptr()
     if o.data_ptr() == x.data_ptr() and o.numel():
-        if o.stride() != x.stride():
-            raise ValueError(f"{name} in place must have its input's shape and strides")
-        return _like(o, name, dtype, x.shape, dev, contiguous=False)
+        if o.stride() != x.stride() or o.shape != x.shape or o.dtype is not dtype:
+            raise ValueError(f"{name} in place must have its input's type, shape and strides")
+        return o.data_ptr()
     return _like(o, name, dtype, x.shape, dev)
 
 
@@ -728,34 +747,37 @@ def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved,
         raise ValueError("q and k must be [P, T, heads, dh]")
     P, T, heads, dh = first.shape
     hq = hk = rows = 0
-    q_ptr = k_ptr = v_ptr = qo = ko = vo = slot = None
-    qs = ks = vs = (0, 0)
+    q_ptr = k_ptr = v_ptr = qo = ko = vo = slot = 0
+    qr = qt = kr = kt = vr = vt = 0
     if q is not None:
         hq = heads
-        q_ptr, *qs = _heads4(q, "q", bf, dev)
+        q_ptr, qr, qt = _heads4(q, "q", bf, dev)
         qo = _rope_out(q_out, q, "q_out", bf, dev)
     if k is not None:
         hk = k.shape[2] if k.dim() == 4 else 0
-        k_ptr, *ks = _heads4(k, "k", bf, dev, (P, T, hk, dh))
+        k_ptr, kr, kt = _heads4(k, "k", bf, dev, (P, T, hk, dh))
         if slots is None:
             ko = _rope_out(k_out, k, "k_out", bf, dev)
         else:
-            v_ptr, *vs = _heads4(v, "v", bf, dev, (P, T, hk, dh))
+            v_ptr, vr, vt = _heads4(v, "v", bf, dev, (P, T, hk, dh))
             rows = k_out.numel() // max(P * hk * dh, 1)
             slab = k_out.shape
             cache = slab if len(slab) == 5 and slab[0] == P and slab[3:] == (hk, dh) else (P, rows, hk, dh)
             ko = _like(k_out, "k_cache", bf, cache, dev)
             vo = _like(v_out, "v_cache", bf, cache, dev)
             slot = _like(slots, "slots", torch.int64, (T,), dev)
-    pos = None if positions is None else _like(positions, "positions", torch.int32, (T,), dev)
-    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    pos = 0 if positions is None else _like(positions, "positions", torch.int32, (T,), dev)
+    freq = inv_freq
+    if type(freq) is not np.ndarray or freq.dtype != np.float64 or not freq.flags.c_contiguous:
+        freq = np.ascontiguousarray(freq, dtype=np.float64)
     if freq.ndim != 1:
         raise ValueError("inv_freq must be one-dimensional")
-    a = RopeArgs(q_ptr, k_ptr, v_ptr, qo, ko, vo, pos, slot, freq.__array_interface__["data"][0],
-                 _raw_stream(stream, dev), None if timing is None else timing.handle, T, rows, *qs, *ks, *vs, P, hq, hk, dh,
-                 2 * freq.size, mscale,
-                 (CAAT_ROPE_FLAG_INTERLEAVED if interleaved else 0) | (CAAT_ROPE_FLAG_BACKWARD if backward else 0))
-    _check(lib().caat_rope(a), "caat_rope")
+    code = (_lib or lib()).packed_caat_rope(_PACK_ROPE.pack(
+        q_ptr, k_ptr, v_ptr, qo, ko, vo, pos, slot, freq.__array_interface__["data"][0], _raw_stream(stream, dev),
+        0 if timing is None else timing.handle, T, rows, qr, qt, kr, kt, vr, vt, P, hq, hk, dh, 2 * freq.size, mscale,
+        (CAAT_ROPE_FLAG_INTERLEAVED if interleaved else 0) | (CAAT_ROPE_FLAG_BACKWARD if backward else 0)))
+    if code:
+        _check(code, "caat_rope")
 
 
 def caat_rope(q, k, positions, inv_freq, *, q_out, k_out, interleaved: bool = False, backward: bool = False,
@@ -781,33 +803,23 @@ def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q
     return q_out
 
 
-def _attn_tail(q, k, v, cu_q, cu_k, scale, variant, workspace, stream, timing):
-    """What the forward's and the backward's arguments share: (device, what must outlive the call,
-    addresses of q, k and v, the last fields of the structure)."""
+def _attn_qkv(q, k, v, cu_q, cu_k):
+    """Checks of what the forward and the backward share: (device, what must outlive the call,
+    addresses of q, k and v, addresses and count of the offsets, strides)."""
     dev = _current(q, "q")
     bf = torch.bfloat16
-    q_ptr, *qs = _heads4(q, "q", bf, dev)
-    P, Tq, hq, dh = q.shape
-    k_ptr, *ks = _heads4(k, "k", bf, dev)
-    _, Tk, hk, _ = k.shape
-    v_ptr, *vs = _heads4(v, "v", bf, dev, (P, Tk, hk, dh))
-    if k.shape != v.shape:
+    q_ptr, qr, qt = _heads4(q, "q", bf, dev)
+    k_ptr, kr, kt = _heads4(k, "k", bf, dev)
+    v_ptr, vr, vt = _heads4(v, "v", bf, dev, k.shape)
+    if k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
         raise ValueError("q, k and v must have the same ranks and head size")
     cq, cq_ptr, n = _offsets(cu_q, "cu_q")
-    ck, ck_ptr = None, None
+    ck, ck_ptr = None, 0
     if cu_k is not None:
         ck, ck_ptr, nk = _offsets(cu_k, "cu_k")
         if nk != n:
             raise ValueError("cu_q and cu_k must have the same length")
-    need = 0
-    if workspace is None and (variant != CAAT_VARIANT_ATTN or Tq + 128 * n > _INLINE_QUERIES):
-        need = lib().caat_attn_workspace_size(Tq, Tk, n - 1, P, hq, hk, dh, variant)
-        if need == _SIZE_MAX:
-            need = 0  # sizes the call itself refuses
-    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
-    return dev, (cq, ck, ws), (q_ptr, k_ptr, v_ptr), (
-        cq_ptr, ck_ptr, ws_ptr, ws_bytes, _raw_stream(stream, dev), None if timing is None else timing.handle, Tq, Tk, *qs,
-        *ks, *vs, n - 1, P, hq, hk, dh, dh ** -0.5 if scale is None else scale, 0)
+    return dev, (cq, ck), (q_ptr, k_ptr, v_ptr), (cq_ptr, ck_ptr), n - 1, (qr, qt, kr, kt, vr, vt)
 
 
 def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optional[float] = None, workspace=None,
@@ -818,12 +830,23 @@ def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optiona
     cu_q, cu_k: host offsets [n_seq + 1] of the sequences' queries and keys (cu_k None: cu_q; the last
     query sees the last key); out [P,Tq,heads_q*dh] bf16, the X of caat_rowpar_forward; lse
     [P,heads_q,Tq] fp32, needed by the backward.  scale None: dh ** -0.5."""
-    dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN, workspace, stream, timing)
+    dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     P, Tq, hq, dh = q.shape
-    a = AttnArgs(*qkv, _like(out, "out", torch.bfloat16, (P, Tq, hq * dh), dev),
-                 None if lse is None else _like(lse, "lse", torch.float32, (P, hq, Tq), dev), *tail)
-    _check(lib().caat_attn_forward(a), "caat_attn_forward")
-    del keep
+    Tk, hk = k.shape[1:3]
+    L = _lib or lib()
+    out_ptr = _like(out, "out", torch.bfloat16, (P, Tq, hq * dh), dev)
+    lse_ptr = 0 if lse is None else _like(lse, "lse", torch.float32, (P, hq, Tq), dev)
+    tail = (_raw_stream(stream, dev), 0 if timing is None else timing.handle, Tq, Tk, *strides, n, P, hq, hk, dh,
+            dh ** -0.5 if scale is None else scale, 0)
+    ws, ws_ptr, ws_bytes = (None, 0, 0) if workspace is None else _workspace(workspace, 0, dev, stream)
+    code = L.packed_caat_attn_forward(_PACK_ATTN.pack(*qkv, out_ptr, lse_ptr, *cu, ws_ptr, ws_bytes, *tail))
+    if code == CAAT_ERR_WORKSPACE and workspace is None:  # only long work lists need one
+        need = L.caat_attn_workspace_size(Tq, Tk, n, P, hq, hk, dh, CAAT_VARIANT_ATTN)
+        ws, ws_ptr, ws_bytes = _workspace(None, need, dev, stream)
+        code = L.packed_caat_attn_forward(_PACK_ATTN.pack(*qkv, out_ptr, lse_ptr, *cu, ws_ptr, ws_bytes, *tail))
+    if code:
+        _check(code, "caat_attn_forward")
+    del keep, ws
     return out
 
 
@@ -831,14 +854,27 @@ def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, 
                        workspace=None, stream=None, timing=None):
     """Queues the gradients of caat_attn_forward: dq [P,Tq,heads_q,dh], dk, dv [P,Tk,heads_k,dh] (bf16,
     contiguous) from the forward's inputs, its out and lse, and dout [P,Tq,heads_q*dh]."""
-    dev, keep, qkv, tail = _attn_tail(q, k, v, cu_q, cu_k, scale, CAAT_VARIANT_ATTN_BWD, workspace, stream, timing)
+    dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     bf = torch.bfloat16
     P, Tq, hq, dh = q.shape
-    a = AttnBwdArgs(*qkv, _like(out, "out", bf, (P, Tq, hq * dh), dev), _like(lse, "lse", torch.float32, (P, hq, Tq), dev),
-                    _like(dout, "dout", bf, (P, Tq, hq * dh), dev), _like(dq, "dq", bf, q.shape, dev),
-                    _like(dk, "dk", bf, k.shape, dev), _like(dv, "dv", bf, k.shape, dev), *tail)
-    _check(lib().caat_attn_backward(a), "caat_attn_backward")
-    del keep
+    Tk, hk = k.shape[1:3]
+    L = _lib or lib()
+    need = 0
+    if workspace is None:
+        need = L.caat_attn_workspace_size(Tq, Tk, n, P, hq, hk, dh, CAAT_VARIANT_ATTN_BWD)
+        if need == _SIZE_MAX:
+            need = 0  # sizes the call itself refuses
+    ws, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
+    rows = (P, Tq, hq * dh)
+    code = L.packed_caat_attn_backward(_PACK_ATTN_BWD.pack(
+        *qkv, _like(out, "out", bf, rows, dev), _like(lse, "lse", torch.float32, (P, hq, Tq), dev),
+        _like(dout, "dout", bf, rows, dev), _like(dq, "dq", bf, q.shape, dev), _like(dk, "dk", bf, k.shape, dev),
+        _like(dv, "dv", bf, k.shape, dev), *cu, ws_ptr, ws_bytes, _raw_stream(stream, dev),
+        0 if timing is None else timing.handle, Tq, Tk, *strides, n, P, hq, hk, dh, dh ** -0.5 if scale is None else scale,
+        0))
+    if code:
+        _check(code, "caat_attn_backward")
+    del keep, ws
     return dq, dk, dv
 
 
@@ -850,23 +886,26 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
     sequence, the new token's included), out [P,B,heads_q*dh]: the X of caat_rowpar_forward."""
     bf = torch.bfloat16
     dev = _current(q, "q")
-    q_ptr, *qs = _heads4(q, "q", bf, dev)
+    q_ptr, qr, qt = _heads4(q, "q", bf, dev)
     P, B, hq, dh = q.shape
-    if k_cache.dim() != 5:
-        raise ValueError("k_cache must be [P, B, capacity, heads_k, dh]")
-    cap, hk = k_cache.shape[2:4]
-    cache = (P, B, cap, hk, dh)
-    k_ptr, v_ptr = _like(k_cache, "k_cache", bf, cache, dev), _like(v_cache, "v_cache", bf, cache, dev)
-    need = lib().caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, CAAT_VARIANT_ATTN_DECODE)
-    if need == _SIZE_MAX:
-        need = 0  # sizes the call itself refuses
-    keep, ws_ptr, ws_bytes = _workspace(workspace, need, dev, stream)
-    a = AttnDecodeArgs(q_ptr, k_ptr, v_ptr, _like(lens, "lens", torch.int32, (B,), dev),
-                       _like(out, "out", bf, (P, B, hq * dh), dev), ws_ptr, ws_bytes, _raw_stream(stream, dev),
-                       None if timing is None else timing.handle, B, cap, *qs, P, hq, hk, dh,
-                       dh ** -0.5 if scale is None else scale, 0)
-    _check(lib().caat_attn_decode(a), "caat_attn_decode")
-    del keep
+    cache = k_cache.shape
+    if len(cache) != 5 or cache[0] != P or cache[1] != B or cache[4] != dh:
+        raise ValueError(f"k_cache must be [{P}, {B}, capacity, heads_k, {dh}], not {tuple(cache)}")
+    cap, hk = cache[2], cache[3]
+    L = _lib or lib()
+    head = (q_ptr, _like(k_cache, "k_cache", bf, cache, dev), _like(v_cache, "v_cache", bf, cache, dev),
+            _like(lens, "lens", torch.int32, (B,), dev), _like(out, "out", bf, (P, B, hq * dh), dev))
+    tail = (_raw_stream(stream, dev), 0 if timing is None else timing.handle, B, cap, qr, qt, P, hq, hk, dh,
+            dh ** -0.5 if scale is None else scale, 0)
+    ws, ws_ptr, ws_bytes = (None, 0, 0) if workspace is None else _workspace(workspace, 0, dev, stream)
+    code = L.packed_caat_attn_decode(_PACK_ATTN_DECODE.pack(*head, ws_ptr, ws_bytes, *tail))
+    if code == CAAT_ERR_WORKSPACE and workspace is None:  # only few or very long sequences need one
+        need = L.caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, CAAT_VARIANT_ATTN_DECODE)
+        ws, ws_ptr, ws_bytes = _workspace(None, need, dev, stream)
+        code = L.packed_caat_attn_decode(_PACK_ATTN_DECODE.pack(*head, ws_ptr, ws_bytes, *tail))
+    if code:
+        _check(code, "caat_attn_decode")
+    del ws
     return out
 
 

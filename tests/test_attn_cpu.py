@@ -180,6 +180,14 @@ def test_workspace_size_refuses(L):
             C.caat_attn_workspace_size(*args)
 
 
+def test_packed_arguments_are_the_structures(L):
+    """The packed form of each call's arguments lays every field where the structure has it."""
+    for name, (packed, args) in C._PACKED.items():
+        values = [i + 1 for i in range(len(args._fields_))]
+        a = args.from_buffer_copy(packed.pack(*values))
+        assert [getattr(a, f) for f, *_ in args._fields_] == values, name
+
+
 def test_binding_refuses_cpu_tensors_and_odd_layouts(L):
     q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     freq, _ = C.caat_rope_frequencies(64)
@@ -196,6 +204,7 @@ def test_binding_refuses_cpu_tensors_and_odd_layouts(L):
     with pytest.raises(TypeError):
         C._heads4(q.float(), "q", torch.bfloat16, -1)
     assert C._heads4(q[:, 1:, :1], "q", torch.bfloat16, -1)[1:] == (4 * 128, 128)
+    assert C._heads4(q, "q", torch.bfloat16, -1)[1:] == (0, 0)
     for good in ([0, 4], (0, 4), np.array([0, 4]), np.array([9, 0, 4, 7], dtype=np.int32)[1:3], torch.tensor([0, 4])):
         keep, ptr, n = C._offsets(good, "cu_q")
         assert n == 2 and list((ctypes.c_int32 * 2).from_address(ptr)) == [0, 4] and keep is not None
