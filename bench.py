@@ -1,7 +1,7 @@
 """Benchmark of the partially synchronized row-parallel FC2 (7B shape) on B200.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl caat|reference]
-                    [--workload fc2-7b|fc2-1b|tiny] [--p 0.5] [--sweep]
+                    [--workload fc2-7b|fc2-1b|tiny] [--p 0.5] [--sweep] [--attn [--backward]]
 
 One step = one call of caat_rowpar_forward on one batch of synthetic input: the P partial
 GEMMs, the partial channel-reduce, the private scale, the residual add and the per-rank
@@ -650,6 +650,90 @@ def run_tp(args):
         "gpu_launches": (3 if args.tp_peer else 2) * args.steps, "device_status": status}))
 
 
+ATTN_BLOCK = {"T": 8192, "P": 8, "heads": 4, "dh": 128}   # per rank: 32 heads of 128 in all (attn-out-7b's input)
+
+
+def attn_block_flops(T, P, heads, dh, H, backward):
+    """Attention over one causal sequence (4 dh per visible pair forward, 10 dh backward) and the
+    output projection (2 T K H forward, 4 T K H backward)."""
+    pairs = P * heads * T * (T + 1) / 2
+    K = P * heads * dh
+    return ((10 if backward else 4) * dh * pairs, (4.0 if backward else 2.0) * T * K * H)
+
+
+def run_attn(args):
+    """The attention block in front of the attn-out-7b projection on one GPU: rotation, causal
+    attention over one sequence, the partially synchronized projection (with --backward: their
+    gradients in reverse).  CUDA events around each call; inputs far larger than L2."""
+    import torch
+    from partial_activation_sync_caat_b200 import build as B
+    from partial_activation_sync_caat_b200 import caat as C
+    from partial_activation_sync_caat_b200 import inputs as I
+    B.build()
+    torch.cuda.set_device(0)
+    T = args.tokens or ATTN_BLOCK["T"]
+    P, heads, dh, H = ATTN_BLOCK["P"], ATTN_BLOCK["heads"], ATTN_BLOCK["dh"], WORKLOADS["attn-out-7b"][2]
+    p = args.p if args.p is not None else WORKLOADS["attn-out-7b"][4]
+    K = P * heads * dh
+    d = I.make_rowpar_inputs(T, K, H, P, seed=rank_seed(0), device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(rank_seed(0) + 1)
+
+    def draw(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda").to(torch.bfloat16)
+
+    q, k, v = (draw(P, T, heads, dh) for _ in range(3))
+    freq, _ = C.caat_rope_frequencies(dh)
+    qr, kr, X, h, out = torch.empty_like(q), torch.empty_like(k), torch.empty_like(d["X"]), torch.empty_like(d["R"]), torch.empty_like(d["R"])
+    lse = torch.empty(P, heads, T, dtype=torch.float32, device="cuda")
+    ws = C.alloc_workspace(C.caat_workspace_size(T, K, H, P))
+    forward = [
+        ("rope", lambda: C.caat_rope(q, k, None, freq, q_out=qr, k_out=kr)),
+        ("attention", lambda: C.caat_attn_forward(qr, kr, v, [0, T], X, lse=lse)),
+        ("projection", lambda: C.caat_rowpar_forward(X, d["W"], d["R"], d["gamma"], None, P, p, out, workspace=ws, h_out=h)),
+    ]
+    stages = forward
+    if args.backward:
+        for _, f in forward:
+            f()
+        dout, dX, dW = draw(P, T, H), torch.empty_like(X), torch.empty_like(d["W"])
+        dgamma = torch.empty(H, dtype=torch.float32, device="cuda")
+        dq, dk, dv, dq0, dk0 = (torch.empty_like(x) for x in (q, k, v, q, k))
+        wb = C.alloc_workspace(C.caat_workspace_size(T, K, H, P, C.CAAT_VARIANT_ROWPAR_BWD))
+        wa = C.alloc_workspace(C.caat_attn_workspace_size(T, T, 1, P, heads, heads, dh, C.CAAT_VARIANT_ATTN_BWD))
+        stages = [
+            ("projection", lambda: C.caat_rowpar_backward(X, d["W"], h, d["gamma"], dout, None, P, p, dX, dW, dgamma, workspace=wb)),
+            ("attention", lambda: C.caat_attn_backward(qr, kr, v, X, lse, dX, [0, T], dq, dk, dv, workspace=wa)),
+            ("rope", lambda: C.caat_rope(dq, dk, None, freq, q_out=dq0, k_out=dk0, backward=True)),
+        ]
+    for _ in range(args.warmup):
+        for _, f in stages:
+            f()
+    torch.cuda.synchronize()
+    clocks = ClockSampler(0)
+    clocks.start()
+    marks = [[torch.cuda.Event(enable_timing=True) for _ in range(len(stages) + 1)] for _ in range(args.steps)]
+    for ev in marks:
+        ev[0].record()
+        for e, (_, f) in zip(ev[1:], stages):
+            f()
+            e.record()
+    torch.cuda.synchronize()
+    seen = clocks.stop()
+    status = C.caat_get_device_status()
+    ms = sum(ev[0].elapsed_time(ev[-1]) for ev in marks) / args.steps
+    parts = {n: round(statistics.median(ev[i].elapsed_time(ev[i + 1]) for ev in marks), 4) for i, (n, _) in enumerate(stages)}
+    fa, fp = attn_block_flops(T, P, heads, dh, H, args.backward)
+    print(json.dumps({
+        "metric": f"TFLOP/s of the attention block{' backward' if args.backward else ''} (rope, causal attention, partially synced projection)",
+        "value": round((fa + fp) / ms / 1e9, 2), "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": round(ms, 4), "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16",
+        "data": "synthetic",
+        "config": {"workload": f"one causal sequence T={T}, {P * heads} heads of {dh} over P={P} ranks, projection to H={H}, p={p}",
+                   "l2": "inputs larger than L2"},
+        "stages_ms": parts, "attention_tflops": round(fa / parts["attention"] / 1e9, 1), "clocks": seen,
+        "device_status": status}))
+
+
 def run_caat(args):
     import torch
     import torch.distributed as dist
@@ -958,6 +1042,9 @@ def main():
     ap.add_argument("--sweep", action="store_true", help="also time p in {0,.25,.5,.75,1}")
     ap.add_argument("--backward", action="store_true",
                     help="time the layer's backward (caat_rowpar_backward) instead of the forward")
+    ap.add_argument("--attn", action="store_true",
+                    help="the attention block in front of the attn-out-7b projection: rotation, causal attention, "
+                         "projection (with --backward: their gradients)")
     ap.add_argument("--tp", action="store_true",
                     help="the layer over real devices: one tensor-parallel rank per GPU (P = --gpus), NCCL "
                          "all-reduce of the shared channels")
@@ -974,6 +1061,8 @@ def main():
         args.warmup = 3
     if args.impl == "reference":
         run_reference(args)
+    elif args.attn:
+        run_attn(args)
     elif args.tp:
         run_tp(args)
     else:

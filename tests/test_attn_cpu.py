@@ -214,3 +214,11 @@ def test_binding_refuses_cpu_tensors_and_odd_layouts(L):
     for big in ([0, 2**31], np.array([0, 2**31])):
         with pytest.raises(C.CaatError):
             C._offsets(big, "cu_q")
+
+
+def test_bench_counts_the_attention_blocks_work():
+    import bench
+    T, P, heads, dh, H = 3, 2, 2, 8, 16
+    visible = sum(i + 1 for i in range(T)) * P * heads
+    assert bench.attn_block_flops(T, P, heads, dh, H, False) == (4 * dh * visible, 2.0 * T * (P * heads * dh) * H)
+    assert bench.attn_block_flops(T, P, heads, dh, H, True) == (10 * dh * visible, 4.0 * T * (P * heads * dh) * H)
