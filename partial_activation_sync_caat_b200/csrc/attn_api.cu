@@ -43,7 +43,8 @@ using caat::host::Recorder;
 
 constexpr size_t kDecodeCounters = 2048;  // 4 bytes per CTA
 static_assert(caat::KD_CTAS * 4 <= kDecodeCounters, "one counter per CTA");
-constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a buffer, rows of a cache
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a buffer, rows of a sequence's cache
+constexpr int64_t kMaxCacheRows = int64_t(1) << 36;  // of all sequences: far more than fit the memory
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -392,6 +393,7 @@ caat_status caat_rope(const caat_rope_args* a) {
   if (a->T > kMaxRows || a->heads_q > 1024 || a->heads_k > 1024) return CAAT_ERR_UNSUPPORTED;
   const bool append = a->slots != nullptr;
   if (append && (a->cache_rows < 0 || a->heads_k == 0)) return CAAT_ERR_INVALID_ARG;
+  if (append && a->cache_rows > kMaxCacheRows) return CAAT_ERR_UNSUPPORTED;
   if (!a->inv_freq) return CAAT_ERR_INVALID_ARG;
   for (int j = 0; j < a->rot / 2; ++j)
     if (!std::isfinite(a->inv_freq[j])) return CAAT_ERR_INVALID_ARG;
@@ -399,7 +401,10 @@ caat_status caat_rope(const caat_rope_args* a) {
 
   static thread_local caat::RopeParams prm;
   std::memset(&prm, 0, sizeof(prm));
-  Range in[3], out[3];
+  Range in[5], out[3];
+  View read[3];  // the tensors of in[], their rows, and whether they are turned in place
+  int64_t row_of[3];
+  bool written[3];
   int n_in = 0, n_out = 0;
   auto tensor = [&](caat::RopeTensor* x, const caat_bf16* p, caat_bf16* o, int64_t s_rank, int64_t s_tok, int heads,
                     bool to_cache) -> caat_status {
@@ -409,16 +414,19 @@ caat_status caat_rope(const caat_rope_args* a) {
     if (!o) return CAAT_ERR_INVALID_ARG;
     if (!aligned16(o)) return CAAT_ERR_UNSUPPORTED;
     const int64_t row = int64_t(heads) * a->dh, rows = to_cache ? a->cache_rows : a->T;
-    const bool in_place = o == p && !to_cache;
+    const bool same = o == p && !to_cache;
     x->in = reinterpret_cast<const __nv_bfloat16*>(p);
     x->out = reinterpret_cast<__nv_bfloat16*>(o);
     x->in_rank = v.rank;
     x->in_tok = v.tok;
-    x->out_rank = in_place ? v.rank : rows * row;
-    x->out_tok = in_place ? v.tok : row;
+    x->out_rank = same ? v.rank : rows * row;
+    x->out_tok = same ? v.tok : row;
     x->heads = heads;
+    read[n_in] = v;
+    row_of[n_in] = row;
+    written[n_in] = same;
     in[n_in++] = range_of(v);
-    if (!in_place) out[n_out++] = range_of(o, static_cast<size_t>(a->P) * rows * row * 2);
+    if (!same) out[n_out++] = range_of(o, static_cast<size_t>(a->P) * rows * row * 2);
     return CAAT_OK;
   };
   caat_status s = CAAT_OK;
@@ -427,11 +435,29 @@ caat_status caat_rope(const caat_rope_args* a) {
     s = tensor(&prm.k, a->k, a->k_out, a->k_stride_rank, a->k_stride_token, a->heads_k, append);
   if (s == CAAT_OK && append) s = tensor(&prm.v, a->v, a->v_out, a->v_stride_rank, a->v_stride_token, a->heads_k, true);
   if (s != CAAT_OK) return s;
-  if (append && a->cache_rows > (int64_t(1) << 40)) return CAAT_ERR_UNSUPPORTED;
+  for (int i = 0; i < n_in; ++i) {
+    if (!written[i]) continue;
+    // in place: no row may lie on another one, of this tensor or of the others
+    const View& w = read[i];
+    if (a->P > 1 && w.rank < (a->T - 1) * w.tok + row_of[i] && w.tok < (a->P - 1) * w.rank + row_of[i]) return CAAT_ERR_INVALID_ARG;
+    for (int j = 0; j < n_in; ++j) {
+      if (j == i || !meet(in[i], in[j])) continue;
+      // slices of one projection: side by side within the same tokens
+      const View& r = read[j];
+      if (w.tok != r.tok || (a->P > 1 && w.rank != r.rank)) return CAAT_ERR_INVALID_ARG;
+      const int64_t d = (r.p - w.p) % w.tok, ahead = d < 0 ? d + w.tok : d;
+      if (ahead < row_of[i] || ahead + row_of[j] > w.tok) return CAAT_ERR_INVALID_ARG;
+    }
+    out[n_out++] = in[i];
+  }
+  const int tensors = n_in;
+  if (a->positions) in[n_in++] = range_of(a->positions, size_t(a->T) * 4);
+  if (append) in[n_in++] = range_of(a->slots, size_t(a->T) * 8);
+  const int apart = n_out - static_cast<int>(std::count(written, written + tensors, true));
   for (int o = 0; o < n_out; ++o) {
-    for (int i = 0; i < n_in; ++i)
+    for (int i = o < apart ? 0 : tensors; i < n_in; ++i)  // (in place against the tensors: above)
       if (meet(out[o], in[i])) return CAAT_ERR_INVALID_ARG;
-    for (int i = 0; i < o; ++i)
+    for (int i = 0; i < std::min(o, apart); ++i)
       if (meet(out[o], out[i])) return CAAT_ERR_INVALID_ARG;
   }
   if ((reinterpret_cast<uintptr_t>(a->positions) & 3u) || (reinterpret_cast<uintptr_t>(a->slots) & 7u))
@@ -528,7 +554,7 @@ caat_status caat_attn_backward(const caat_attn_bwd_args* a) {
   if ((s = check_offsets(a->cu_q, a->n_seq, a->Tq)) != CAAT_OK) return s;
   if ((s = check_offsets(cu_k, a->n_seq, a->Tk)) != CAAT_OK) return s;
   View q, k, v;
-  Range in[5], out[3];
+  Range in[6], out[3];
   int n_in = 0, n_out = 0;
   if (a->Tq > 0) {
     if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
@@ -539,6 +565,7 @@ caat_status caat_attn_backward(const caat_attn_bwd_args* a) {
     in[n_in++] = range_of(q);
     in[n_in++] = range_of(a->out, bytes);
     in[n_in++] = range_of(a->dout, bytes);
+    in[n_in++] = range_of(a->lse, size_t(a->P) * a->Tq * a->heads_q * 4);
     out[n_out++] = range_of(a->dq, bytes);
   }
   if (a->Tk > 0) {
@@ -574,7 +601,7 @@ caat_status caat_attn_decode(const caat_attn_decode_args* a) {
   caat_status s = check_heads(a->P, a->heads_q, a->heads_k, a->dh, a->scale);
   if (s != CAAT_OK) return s;
   if (a->B < 0 || a->capacity < 0 || a->flags != 0) return CAAT_ERR_INVALID_ARG;
-  if (a->capacity > kMaxRows || a->B > caat::KD_MAX_B) return CAAT_ERR_UNSUPPORTED;
+  if (a->capacity > kMaxRows || a->B > caat::KD_MAX_B || a->B * a->capacity > kMaxCacheRows) return CAAT_ERR_UNSUPPORTED;
   if (a->B == 0) return CAAT_OK;
   View q;
   if ((s = make_view(&q, a->q, a->q_stride_rank, a->q_stride_token, a->P, a->B, a->heads_q, a->dh)) != CAAT_OK) return s;

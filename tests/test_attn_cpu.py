@@ -117,6 +117,26 @@ def test_rope_refuses(L):
     assert rope(L, heads_q=0, heads_k=0) == C.CAAT_OK
 
 
+def test_rope_refuses_what_overlaps(L):
+    # positions or slots inside an output
+    assert rope(L, positions=0x300000) == C.CAAT_ERR_INVALID_ARG
+    assert rope(L, q_out=0x100000, positions=0x100100) == C.CAAT_ERR_INVALID_ARG
+    cache = dict(v=0x500000, v_out=0x600000, cache_rows=4)
+    assert rope(L, slots=0x400008, **cache) == C.CAAT_ERR_INVALID_ARG
+    # in place: q and k on one buffer, on each other's rows, with strides of their own
+    assert rope(L, q_out=0x100000, k=0x100000, k_out=0x100000) == C.CAAT_ERR_INVALID_ARG
+    assert rope(L, q_out=0x100000, k=0x100000) == C.CAAT_ERR_INVALID_ARG
+    fused = dict(q_out=0x100000, q_stride_token=768, q_stride_rank=7680, k_stride_token=768, k_stride_rank=7680)
+    for k in (0x100000 + 2 * 504, 0x100000 + 2 * 520, 0x100000 - 2 * 248):
+        assert rope(L, k=k, k_out=k, **fused) == C.CAAT_ERR_INVALID_ARG, hex(k)
+    k = 0x100000 + 2 * 512
+    assert rope(L, k=k, k_out=k, **{**fused, "k_stride_token": 776, "k_stride_rank": 7760}) == C.CAAT_ERR_INVALID_ARG
+    # ranks that share rows
+    assert rope(L, q_out=0x100000, q_stride_token=512, q_stride_rank=512) == C.CAAT_ERR_INVALID_ARG
+    # a cache beyond any memory
+    assert rope(L, slots=0x8000, v=0x500000, v_out=0x600000, cache_rows=1 << 62) == C.CAAT_ERR_UNSUPPORTED
+
+
 def attn(L, name="caat_attn_forward", **kw):
     cu = np.array([0, 100, 300], dtype=np.int32)
     a = fill(C.AttnArgs() if name == "caat_attn_forward" else C.AttnBwdArgs(), q=0x1000000, k=0x2000000, v=0x3000000,
@@ -147,7 +167,7 @@ def test_attention_refuses(L, name):
         assert attn(L, lse=0x4000000) == C.CAAT_ERR_INVALID_ARG   # lse on out
     else:
         for kw in (dict(dout=None), dict(lse=None), dict(dq=None), dict(dk=None), dict(dv=None), dict(dq=0x1000000),
-                   dict(dk=0x9000000, dv=0x9000010), dict(dk=0x7000000)):
+                   dict(dk=0x9000000, dv=0x9000010), dict(dk=0x7000000), dict(dq=0x5000000)):
             assert attn(L, name, **kw) == C.CAAT_ERR_INVALID_ARG, kw
         assert attn(L, name, workspace=None) == C.CAAT_ERR_WORKSPACE
         assert attn(L, name, ws_bytes=256) == C.CAAT_ERR_WORKSPACE
@@ -166,7 +186,7 @@ def test_decode_refuses(L):
                dict(k_cache=None), dict(v_cache=None), dict(lens=None), dict(out=None), dict(out=0x1000000), dict(out=0x10000010)):
         assert decode(L, **kw) == C.CAAT_ERR_INVALID_ARG, kw
     for kw in (dict(dh=132), dict(dh=136), dict(k_cache=0x10000008), dict(lens=0x3000002), dict(B=65536),
-               dict(capacity=(1 << 30) + 1)):
+               dict(capacity=(1 << 30) + 1), dict(B=4096, capacity=1 << 30)):
         assert decode(L, **kw) == C.CAAT_ERR_UNSUPPORTED, kw
     for kw in (dict(workspace=None), dict(ws_bytes=1024), dict(workspace=0x6000010)):
         assert decode(L, **kw) == C.CAAT_ERR_WORKSPACE, kw
