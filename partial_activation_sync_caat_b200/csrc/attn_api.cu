@@ -344,7 +344,8 @@ caat_status launch_attn_backward(const caat_attn_bwd_args* a, const int32_t* cu_
     if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
     rec.after_kernel(a->stream);
     if (L.splits > 1) {
-      caat::attn_dkv_join_kernel<<<dim3(static_cast<unsigned>(jobs.size()), P, 4), 256, 0, a->stream>>>(prm);
+      const int pieces = (caat::KA_TILE * hk * dh / 4 + 255) / 256;
+      caat::attn_dkv_join_kernel<<<dim3(static_cast<unsigned>(jobs.size()), P, 2 * std::min(pieces, 1024)), 256, 0, a->stream>>>(prm);
       if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
       rec.after_kernel(a->stream);
     }

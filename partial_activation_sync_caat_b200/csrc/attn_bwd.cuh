@@ -657,23 +657,24 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// dk, dv of a job's keys from the partial sums, added in the order of the splits.
+// dk, dv of a job's keys from the partial sums, added in the order of the splits.  Each thread has one
+// 16-byte piece of dk or dv, four splits' loads in flight (packed 4096 tokens, 4 ranks of one key head of 64,
+// 3 splits, 25 MB: 9.3 to 10.2 us between events; with two pieces a thread, one after another, 11.1).
 __global__ void __launch_bounds__(256) attn_dkv_join_kernel(const __grid_constant__ BwdAttnParams prm) {
   const AttnJob job = prm.jobs.far ? prm.jobs.far[blockIdx.x] : prm.jobs.near[blockIdx.x];
-  const int rank = blockIdx.y;
+  const int rank = blockIdx.y, w = blockIdx.z & 1;
   const int vecs = prm.hk * prm.dh / 4;  // a key's row over all heads
   const int64_t all = prm.P * prm.Tk * prm.hk * prm.dh;
   const int64_t base = (rank * prm.Tk + job.k0) * prm.hk * prm.dh;
-  for (int i = threadIdx.x + blockIdx.z * 256; i < job.k_rows * vecs; i += 256 * gridDim.z) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int z = 0; z < prm.splits; ++z) {
-        const float4 v = *reinterpret_cast<const float4*>(prm.part + (w * prm.splits + z) * all + base + 4 * i);
-        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-      }
-      *reinterpret_cast<uint2*>((w ? prm.dk : prm.dv) + base + 4 * i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  for (int i = threadIdx.x + (blockIdx.z >> 1) * 256; i < job.k_rows * vecs; i += 256 * (gridDim.z >> 1)) {
+    const float4* src = reinterpret_cast<const float4*>(prm.part + w * prm.splits * all + base) + i;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int z = 0; z < prm.splits; ++z) {
+      const float4 v = __ldcs(src + z * (all / 4));
+      s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
     }
+    *reinterpret_cast<uint2*>((w ? prm.dk : prm.dv) + base + 4 * i) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
   }
 }
 
