@@ -506,7 +506,9 @@ CAAT_API caat_status caat_rope_frequencies(int rot, double theta, int scaling, d
  *   inv_freq   HOST, rot / 2 doubles, finite; read before return
  *   rot        0 < rot <= dh; rot % 16 == 0 (interleaved: rot % 8 == 0)
  *   dh         dh % 8 == 0, dh <= 256
- * Outputs that are not in place must not overlap the inputs.  Pointers 16-byte aligned.
+ * Outputs that are not in place must not overlap the inputs; a tensor turned in place must not share
+ * elements with another one, nor with itself between ranks (slices of one projection do not).  Pointers
+ * 16-byte aligned, positions 4, slots 8.
  */
 typedef struct caat_rope_args {
   const caat_bf16* q;
@@ -587,7 +589,8 @@ CAAT_API caat_status caat_attn_forward(const caat_attn_args* args);
  *   dq [P, Tq, heads_q, dh], dk, dv [P, Tk, heads_k, dh]  device bf16, contiguous (out).  Keys that no
  *               query sees get zeros; rows outside every sequence are not written.
  *   workspace   caat_attn_workspace_size(..., CAAT_VARIANT_ATTN_BWD) bytes, 256-byte aligned
- * Outputs must not overlap the inputs or each other.
+ * Outputs must not overlap the inputs or each other.  Values that are not finite make the gradients of
+ * their own sequence unspecified; they never reach another sequence's.  Capturable as the forward.
  */
 typedef struct caat_attn_bwd_args {
   const caat_bf16* q;
@@ -628,7 +631,8 @@ CAAT_API caat_status caat_attn_backward(const caat_attn_bwd_args* args);
  *                    never used, whatever they hold.
  *   out              device bf16 [P, B, heads_q * dh] contiguous; must not overlap the inputs
  *   workspace        caat_attn_workspace_size(B, capacity, ..., CAAT_VARIANT_ATTN_DECODE) bytes, 256-byte
- *                    aligned; two calls that may overlap on the GPU need one each
+ *                    aligned, NULL when that is 0; two calls that may overlap on the GPU need one each
+ *   B                at most 4096
  *   dh, heads, scale as in caat_attn_forward
  * Deterministic; capturable.
  */
