@@ -1,4 +1,5 @@
-"""Builds libcaat.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libcaat.so (the C-ABI library) in-tree with nvcc for sm_100a, and _marshal.so (the compiled
+half of the Python binding, against PyTorch's headers) with g++.
 
     python -m partial_activation_sync_caat_b200.build [--verbose-ptxas]
 
@@ -7,10 +8,12 @@ run time, and so loads on a machine without a GPU (the ABI tests rely on that).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcaat.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["caat_api.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -33,16 +37,25 @@ def nvcc_path() -> str:
 def _deps():
     files = [os.path.join(INCLUDE, "caat.h")]
     for f in os.listdir(CSRC):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.endswith((".cu", ".cuh", ".h", ".cpp")):
             files.append(os.path.join(CSRC, f))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _marshal_command(out: str) -> list:
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    system = [os.path.join(torch, "include"), sysconfig.get_paths()["include"], cuda]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            *(x for d in system for x in ("-isystem", d)), "-I", INCLUDE, os.path.join(CSRC, "marshal.cpp"), "-o", out,
+            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -58,6 +71,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         for src in SOURCES:
             cmd = base + ["-c", os.path.join(CSRC, src), "-o", os.path.join(objs, src + ".o")]
             jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+        cmd = _marshal_command(MARSHAL + ".tmp")
+        jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         outs = [(cmd, p.communicate()[0], p.returncode) for cmd, p in jobs]
         if all(rc == 0 for _, _, rc in outs):
             cmd = base + ["-shared", "-o", tmp] + [os.path.join(objs, src + ".o") for src in SOURCES]
@@ -69,6 +84,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if verbose_ptxas:
             sys.stderr.write(text)
     os.replace(tmp, LIB)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 

@@ -178,8 +178,8 @@ class AttnDecodeArgs(ctypes.Structure):
     ]
 
 
-# The attention block's calls are short enough for the marshalling to show: their arguments are packed
-# in one go (native layout, the same as the structures above) and passed as bytes.
+# The attention block's calls are short enough for the marshalling to show: ordinary ones go through
+# _marshal.so, the others have their arguments packed in one go (native layout, the same as the structures above) and passed as bytes.
 _PACK_ROPE = struct.Struct("@11P8q5ifI0P")
 _PACK_ATTN = struct.Struct("@5P2PPN2P8q5ifI0P")
 _PACK_ATTN_BWD = struct.Struct("@9P2PPN2P8q5ifI0P")
@@ -189,6 +189,27 @@ _PACKED = {"caat_rope": (_PACK_ROPE, RopeArgs), "caat_attn_forward": (_PACK_ATTN
 
 _SIZE_MAX = ctypes.c_size_t(-1).value
 _lib = None
+_marshal = None  # the compiled marshalling of the attention block's calls, bound to the library
+
+
+def _bind_marshal(L):
+    """Imports _marshal.so and gives it the library's functions.  Built for another PyTorch or not at all,
+    it is left out: the calls are then marshalled here, which takes the host 5 us longer."""
+    global _marshal
+    try:
+        from . import _marshal as m
+    except ImportError:
+        _marshal = None
+        return
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.caat_rope, L.caat_attn_forward, L.caat_attn_backward, L.caat_attn_decode, L.caat_attn_workspace_size)))
+    _marshal = m
+
+
+def _fast():
+    """The compiled marshalling (or None), after the library has been loaded."""
+    lib()
+    return _marshal
 
 
 def lib() -> ctypes.CDLL:
@@ -264,6 +285,7 @@ def lib() -> ctypes.CDLL:
     L.caat_status_string.restype = ctypes.c_char_p
     L.caat_version.argtypes = []
     L.caat_version.restype = ctypes.c_char_p
+    _bind_marshal(L)
     _lib = L
     return L
 
@@ -788,7 +810,14 @@ def caat_rope(q, k, positions, inv_freq, *, q_out, k_out, interleaved: bool = Fa
     inv_freq: host float64 [rot / 2] (caat_rope_frequencies); the first rot elements of a head turn.
     q_out, k_out: contiguous, or q and k themselves (in place).  backward: by the negative angle, the
     gradient of the same call."""
-    _rope(q, k, None, positions, None, inv_freq, q_out, k_out, None, interleaved, backward, mscale, stream, timing)
+    fast = _marshal or _fast()
+    code = None
+    if fast and stream is None and timing is None:
+        code = fast.rope(q, k, None, positions, None, inv_freq, q_out, k_out, None, interleaved, backward, mscale)
+    if code is None:
+        _rope(q, k, None, positions, None, inv_freq, q_out, k_out, None, interleaved, backward, mscale, stream, timing)
+    elif code:
+        _check(code, "caat_rope")
     return q_out, k_out
 
 
@@ -799,7 +828,14 @@ def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q
     position).  Slots outside the cache are skipped and reported by caat_get_device_status."""
     if k is None or v is None or slots is None:
         raise ValueError("caat_rope_append needs k, v and slots")
-    _rope(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, interleaved, backward, mscale, stream, timing)
+    fast = _marshal or _fast()
+    code = None
+    if fast and stream is None and timing is None:
+        code = fast.rope(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, interleaved, backward, mscale)
+    if code is None:
+        _rope(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, interleaved, backward, mscale, stream, timing)
+    elif code:
+        _check(code, "caat_rope")
     return q_out
 
 
@@ -830,6 +866,13 @@ def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optiona
     cu_q, cu_k: host offsets [n_seq + 1] of the sequences' queries and keys (cu_k None: cu_q; the last
     query sees the last key); out [P,Tq,heads_q*dh] bf16, the X of caat_rowpar_forward; lse
     [P,heads_q,Tq] fp32, needed by the backward.  scale None: dh ** -0.5."""
+    fast = _marshal or _fast()
+    if fast and stream is None and timing is None:
+        code = fast.attn_forward(q, k, v, cu_q, cu_k, out, lse, scale, workspace)
+        if code is not None:
+            if code:
+                _check(code, "caat_attn_forward")
+            return out
     dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     P, Tq, hq, dh = q.shape
     Tk, hk = k.shape[1:3]
@@ -854,6 +897,13 @@ def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, 
                        workspace=None, stream=None, timing=None):
     """Queues the gradients of caat_attn_forward: dq [P,Tq,heads_q,dh], dk, dv [P,Tk,heads_k,dh] (bf16,
     contiguous) from the forward's inputs, its out and lse, and dout [P,Tq,heads_q*dh]."""
+    fast = _marshal or _fast()
+    if fast and stream is None and timing is None:
+        code = fast.attn_backward(q, k, v, cu_q, cu_k, out, lse, dout, dq, dk, dv, scale, workspace)
+        if code is not None:
+            if code:
+                _check(code, "caat_attn_backward")
+            return dq, dk, dv
     dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     bf = torch.bfloat16
     P, Tq, hq, dh = q.shape
@@ -884,6 +934,13 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
 
     q [P,B,heads_q,dh], caches [P,B,capacity,heads_k,dh] (bf16), lens CUDA int32 [B] (keys of each
     sequence, the new token's included), out [P,B,heads_q*dh]: the X of caat_rowpar_forward."""
+    fast = _marshal or _fast()
+    if fast and stream is None and timing is None:
+        code = fast.attn_decode(q, k_cache, v_cache, lens, out, scale, workspace)
+        if code is not None:
+            if code:
+                _check(code, "caat_attn_decode")
+            return out
     bf = torch.bfloat16
     dev = _current(q, "q")
     q_ptr, qr, qt = _heads4(q, "q", bf, dev)

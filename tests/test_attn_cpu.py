@@ -236,6 +236,22 @@ def test_binding_refuses_cpu_tensors_and_odd_layouts(L):
             C._offsets(big, "cu_q")
 
 
+def test_compiled_marshalling_leaves_odd_arguments_alone(L):
+    """Without a GPU no tensor is taken: every function hands the call back."""
+    m = C._marshal
+    assert m is not None
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    f = np.ones(32)
+    for x in (q, None, 3, [q]):
+        assert m.rope(x, q, None, None, None, f, q, q, None, False, False, 1.0) is None
+        assert m.attn_forward(x, q, q, [0, 4], None, q, None, None, None) is None
+        assert m.attn_backward(x, q, q, [0, 4], None, q, q, q, q, q, q, None, None) is None
+        assert m.attn_decode(x, q, q, q, q, None, None) is None
+    assert m.rope() is None and m.attn_decode(q) is None
+    with pytest.raises(TypeError):
+        m.bind(1)
+
+
 def test_bench_counts_the_attention_blocks_work():
     import bench
     T, P, heads, dh, H = 3, 2, 2, 8, 16
