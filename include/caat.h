@@ -580,7 +580,9 @@ CAAT_API caat_status caat_attn_forward(const caat_attn_args* args);
 /*
  * caat_attn_backward - gradients of caat_attn_forward.  With P the probabilities (recomputed from lse),
  * D = rowsum(dout * out):
- *   dv = P^T dout,  dS = scale P (dout v^T - D),  dq = dS k,  dk = dS^T q,
+ *   dv = P^T dout,  dS = scale P (dout v^T - D),  dq = dS k,  dk = dS^T q
+ * (of the first queries of a sequence, which see 128 keys at most, D is the sum of P (dout v^T) instead: the
+ * same without the rounding of out),
  * sums in fp32 (over the queries of every head that shares a key head, too, in a fixed order: results
  * do not change from run to run); P and dS are rounded to bf16 as operands of the products.
  *

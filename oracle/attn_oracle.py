@@ -83,7 +83,10 @@ def attention(q, k, v, cu_q, cu_k=None, scale=None):
 def attention_backward(q, k, v, out, lse, dout, cu_q, cu_k=None, scale=None):
     """Gradients from the forward's out and lse as given: dict dq, dk, dv with, for each, `*_abs`
     (the sum of the absolute values of its terms) and for dq, dk `*_wide` (the same with
-    |dP| and |D| replaced by their sums of absolute values, which bounds cancellation)."""
+    |dP| and |D| replaced by their sums of absolute values, which bounds cancellation).
+
+    D = rowsum(dout out).  Of a sequence's queries, taken 128 at a time, those that all see 128 keys at most
+    have the sum of P dP instead, for which the former stands: the stored out has it rounded."""
     q, k, v, out, lse, dout = (_f64(x) for x in (q, k, v, out, lse, dout))
     P, Tq, hq, dh = q.shape
     out, dout = out.reshape(q.shape), dout.reshape(q.shape)
@@ -101,9 +104,16 @@ def attention_backward(q, k, v, out, lse, dout, cu_q, cu_k=None, scale=None):
                 Q, K, V, G = q[r, a:b, h], k[r, c:d, kv], v[r, c:d, kv], dout[r, a:b, h]
                 L = np.where(np.isfinite(lse[r, h, a:b]), lse[r, h, a:b], 0.0)[:, None]
                 W = np.exp(np.where(see, scale * (Q @ K.T) - L, -np.inf))
+                dP, wide_P = G @ V.T, np.abs(G) @ np.abs(V).T
                 D = (G * out[r, a:b, h]).sum(1, keepdims=True)
-                dS = scale * W * (G @ V.T - D)
-                wide = scale * W * (np.abs(G) @ np.abs(V).T + (np.abs(G) * np.abs(out[r, a:b, h])).sum(1, keepdims=True))
+                wide_D = (np.abs(G) * np.abs(out[r, a:b, h])).sum(1, keepdims=True)
+                for i in range(0, b - a, 128):
+                    e = min(i + 128, b - a)
+                    if e + (d - c) - (b - a) <= 128:
+                        D[i:e] = (W[i:e] * dP[i:e]).sum(1, keepdims=True)
+                        wide_D[i:e] = (W[i:e] * wide_P[i:e]).sum(1, keepdims=True)
+                dS = scale * W * (dP - D)
+                wide = scale * W * (wide_P + wide_D)
                 g["dq"][r, a:b, h], g["dq_abs"][r, a:b, h] = dS @ K, np.abs(dS) @ np.abs(K)
                 g["dq_wide"][r, a:b, h] = wide @ np.abs(K)
                 g["dk"][r, c:d, kv] += dS.T @ Q

@@ -46,7 +46,7 @@ struct DqCfg {
   static constexpr int kK = HD == 128 ? 3 : 4;
   static constexpr int kV = HD == 128 ? 2 : 3;
   static constexpr int kSlots = kK + kV;
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + KA_TILE * 4 + 512;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + 2 * KA_TILE * 4 + 512;
   static __device__ __forceinline__ int k_slot(int j) { return j % kK; }
   static __device__ __forceinline__ int v_slot(int j) { return kK + j % kV; }
 };
@@ -65,8 +65,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   uint8_t* sQ = smem;
   uint8_t* sG = smem + Cfg::kTileBytes;
   uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
-  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + KA_TILE);
+  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [2][128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 2 * KA_TILE);
   uint64_t* q_full = bars;
   uint64_t* full = q_full + 1;             // [slots]
   uint64_t* empty = full + Cfg::kSlots;    // [slots]
@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   uint64_t* k_raw = ds_full + 1;           // the last key block has arrived, to be scrubbed
   uint64_t* scrubbed = k_raw + 1;
   uint64_t* dq_done = scrubbed + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(dq_done + 1);
+  uint64_t* d_full = dq_done + 1;          // 8 warps
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(d_full + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -122,6 +123,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     mbar_init(k_raw, 1);
     mbar_init(scrubbed, 1);
     mbar_init(dq_done, 1);
+    mbar_init(d_full, 8);
     fence_mbar_init();
     if (n_blk > 0) {
       mbar_arrive_expect_tx(q_full, 2 * Cfg::kTileBytes);
@@ -131,8 +133,12 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       load_kv(1);
     }
   }
+  // Where one block holds all keys that the tile sees, the sum of p dP over it is D without the rounding of
+  // the stored output, whose share of the error is largest in such rows (dq of 5 to 2048 tokens off by
+  // 0.0025 relative without this, 0.0024 with; the rounding of dq itself is 0.0017).
+  const bool one = n_blk == 1;
   uint4 d_o[8], d_g[8];  // 16 lanes a row, a warp 16 rows
-  if (warp < 8) {
+  if (warp < 8 && !one) {
     const int e = 8 * (lane & 15);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -245,27 +251,30 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const bool mine = row < job.rows;
     const int64_t grow = job.q0 + row;
     const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
-    // D: a row a lane, the loads touched 32 rows each and took 12,000 clocks
+    float D = 0.f;
+    if (!one) {
+      // D: a row a lane, the loads touched 32 rows each and took 12,000 clocks
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t wa[4] = {d_o[i].x, d_o[i].y, d_o[i].z, d_o[i].w}, wb[4] = {d_g[i].x, d_g[i].y, d_g[i].z, d_g[i].w};
-      float part = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t wa[4] = {d_o[i].x, d_o[i].y, d_o[i].z, d_o[i].w}, wb[4] = {d_g[i].x, d_g[i].y, d_g[i].z, d_g[i].w};
+        float part = 0.f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
-        part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
+        for (int u = 0; u < 4; ++u) {
+          part = fmaf(bf16lo(wa[u]), bf16lo(wb[u]), part);
+          part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+        if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
       }
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
-      if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      D = sD[row];
+      if (mine && w == 0) prm.D[srow] = D;
     }
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float D = sD[row];
-    if (mine && w == 0) prm.D[srow] = D;
     const float c = prm.scale * KA_LOG2E;
     float nl = mine ? -prm.lse[srow] * KA_LOG2E : 0.f;
     if (nl == INFINITY) nl = 0.f;  // a row that sees no key: all its scores are masked
-    const uint64_t c2 = pack_f32x2(c, c), nl2 = pack_f32x2(nl, nl), nd2 = pack_f32x2(-D, -D);
+    const uint64_t c2 = pack_f32x2(c, c), nl2 = pack_f32x2(nl, nl);
     const int vis = job.first + row;
     bool ok = true;
     for (int j = 0; j < n_blk; ++j) {
@@ -293,14 +302,32 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
           g[y] = y < seen ? g[y] : 0u;
         }
       }
+      auto prob = [&](int y) {
+        float a, b;
+        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, nl2), a, b);
+        return pack_f32x2(ex2(a), ex2(b));
+      };
+      auto dp = [&](int y) { return pack_f32x2(__uint_as_float(g[2 * y]), __uint_as_float(g[2 * y + 1])); };
+      if (one) {
+        uint64_t sum2 = 0;
+        float a, b;
+#pragma unroll
+        for (int y = 0; y < 32; ++y) sum2 = fma_f32x2(prob(y), dp(y), sum2);
+        unpack_f32x2(sum2, a, b);
+        sD[w * KA_TILE + row] = a + b;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_full);
+        ok = warp_wait(d_full, 0, tmo, 122);
+        if (!ok) break;
+        D = sD[row] + sD[KA_TILE + row];
+        if (mine && w == 0) prm.D[srow] = D;
+      }
+      const uint64_t nd2 = pack_f32x2(-D, -D);
       uint32_t p[32];
 #pragma unroll
       for (int y = 0; y < 32; ++y) {
-        float a, b, x0, x1;
-        unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])), c2, nl2), a, b);
-        unpack_f32x2(mul_f32x2(pack_f32x2(ex2(a), ex2(b)),
-                               add_f32x2(pack_f32x2(__uint_as_float(g[2 * y]), __uint_as_float(g[2 * y + 1])), nd2)),
-                     x0, x1);
+        float x0, x1;
+        unpack_f32x2(mul_f32x2(prob(y), add_f32x2(dp(y), nd2)), x0, x1);
         p[y] = pack_bf16x2(x0, x1);
       }
       tmem_st_32x32b_x32(lanes + kDS + (j & 1) * 64 + 32 * w, p);

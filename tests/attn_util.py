@@ -12,7 +12,9 @@ forward   p off by at most 2 s + 2 e relative (numerator and sum), p rounded to 
           |lse - ref| <= s + e + 2^-23 |ref|
 backward  (from the forward's out and lse as stored) P off by s + e relative, rounded to bf16 for dv
           (u); dS = scale P (dP - D) off by (s + e) |dS| and by the fp32 sums in dP and D,
-          (dh + 2) 2^-23 of their sums of absolute values ("wide"), and rounded to bf16 (u)."""
+          (dh + 2) 2^-23 of their sums of absolute values ("wide"), and rounded to bf16 (u).  Where D is the sum
+          of P dP, with P off by s + e, it is off by (s + e) sum P |dP| more, and |dP| is at most its sum of
+          absolute values: (s + e) of the part of "wide" that stands for D."""
 import numpy as np
 
 from oracle import caat_oracle as O
@@ -62,6 +64,6 @@ def check_grads(got, ref, M, dh, what=""):
         g, r = O._f64(got[name]), ref[name]
         bound = (U + (1 + U) * (s + _e(ref["n"]))) * ref[name + "_abs"] + U * np.abs(r) + 1e-30
         if name != "dv":
-            bound = bound + (1 + U) * (dh + 2) * 2.0 ** -22 * ref[name + "_wide"]
+            bound = bound + (1 + U) * ((dh + 2) * 2.0 ** -22 + s + _e(ref["n"])) * ref[name + "_wide"]
         rows = ~np.isnan(r).any(axis=(0, 2, 3))
         _check(g[:, rows], r[:, rows], bound[:, rows], f"{name} {what}")
