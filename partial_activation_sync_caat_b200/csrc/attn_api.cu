@@ -482,8 +482,9 @@ caat_status caat_rope(const caat_rope_args* a) {
   const int per_head = a->rot / (inter ? 8 : 16) + (a->dh - a->rot) / 8;
   const int64_t items = int64_t(a->P) * ((prm.q.heads + prm.k.heads) * per_head + prm.v.heads * (a->dh / 8));
   // Two items a thread keep more loads in flight for many tokens; for few, one a thread spreads them over
-  // more SMs.
-  const bool few = a->T * ((items + 511) / 512) < 4 * int64_t(sms);
+  // more SMs, and where a token has no more than 256 the second would be nobody's (T=3001, 176 items a
+  // token: 8.2 us | 9.1).
+  const bool few = items <= caat::KR_THREADS || a->T * ((items + 511) / 512) < 4 * int64_t(sms);
   const int per_cta = caat::KR_THREADS * (few ? 1 : 2);
   const unsigned gy = static_cast<unsigned>((items + per_cta - 1) / per_cta);
   const unsigned gx = static_cast<unsigned>(std::min<int64_t>(a->T, std::max<int64_t>(1, (caat::KR_CTAS * int64_t(sms) + gy - 1) / gy)));
