@@ -309,12 +309,15 @@ caat_status launch_attn_backward(const caat_attn_bwd_args* a, const int32_t* cu_
   }
   const int64_t Tq = a->Tq ? a->Tq : 1, Tk = a->Tk ? a->Tk : 1;
   const int hq_m = a->Tq ? hq : 1, hk_m = a->Tk ? hk : 1;
-  CUtensorMap mq, mg, mk, mv, mq64, mg64;
+  CUtensorMap mq, mg, mk, mv, mq64, mg64, mk64, mv64;
   if ((s = heads_map(&mq, any, P, Tq, hq_m, dh)) != CAAT_OK || (s = heads_map(&mg, g, P, Tq, hq_m, dh)) != CAAT_OK ||
       (s = heads_map(&mk, a->Tk ? k : any, P, Tk, hk_m, dh)) != CAAT_OK ||
       (s = heads_map(&mv, a->Tk ? v : any, P, Tk, hk_m, dh)) != CAAT_OK ||
       (s = heads_map(&mq64, any, P, Tq, hq_m, dh, caat::KB2_QT)) != CAAT_OK ||
       (s = heads_map(&mg64, g, P, Tq, hq_m, dh, caat::KB2_QT)) != CAAT_OK)
+    return s;
+  if (dh <= 64 && ((s = heads_map(&mk64, a->Tk ? k : any, P, Tk, hk_m, dh, caat::DqCfg<64>::kKeys)) != CAAT_OK ||
+                   (s = heads_map(&mv64, a->Tk ? v : any, P, Tk, hk_m, dh, caat::DqCfg<64>::kKeys)) != CAAT_OK))
     return s;
   Recorder rec;
   rec.begin(a->timing, a->stream);
@@ -325,9 +328,9 @@ caat_status launch_attn_backward(const caat_attn_bwd_args* a, const int32_t* cu_
     if (grid > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
     if ((s = place_jobs(jobs, &prm.jobs, ws + L.q_list, a->stream)) != CAAT_OK) return s;
     if (dh <= 64)
-      caat::attn_dq_kernel<64><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DqCfg<64>::kSmem, a->stream>>>(mq, mg, mk, mv, prm);
+      caat::attn_dq_kernel<64><<<static_cast<unsigned>(grid), caat::DqCfg<64>::kThreads, caat::DqCfg<64>::kSmem, a->stream>>>(mq, mg, mk64, mv64, prm);
     else
-      caat::attn_dq_kernel<128><<<static_cast<unsigned>(grid), caat::KB2_THREADS, caat::DqCfg<128>::kSmem, a->stream>>>(mq, mg, mk, mv, prm);
+      caat::attn_dq_kernel<128><<<static_cast<unsigned>(grid), caat::DqCfg<128>::kThreads, caat::DqCfg<128>::kSmem, a->stream>>>(mq, mg, mk, mv, prm);
     if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
     rec.after_kernel(a->stream);
   }

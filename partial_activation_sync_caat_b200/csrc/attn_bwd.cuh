@@ -19,7 +19,7 @@
 
 namespace caat {
 
-constexpr int KB2_THREADS = 384;  // warps 0-7: elementwise, 8: MMA, 9: TMA, 10: scrubbing, 11: idle
+constexpr int KB2_THREADS = 384;  // dkv: warps 0-7 elementwise, 8 MMA, 9 TMA, 10 scrubbing, 11 idle
 constexpr int KB2_QT = 64;        // queries per step of the dkv kernel
 
 struct BwdAttnParams {
@@ -41,22 +41,35 @@ struct BwdAttnParams {
 template <int HD>
 struct DqCfg {
   static constexpr int kBoxes = HD / 64;
-  static constexpr int kTileBytes = kBoxes * KA_BOX_BYTES;
+  static constexpr int kTileBytes = kBoxes * KA_BOX_BYTES;        // Q or dO: 128 queries
+  static constexpr int kKeys = HD;                                // keys of a block
+  static constexpr int kBox = kKeys * 128;                        // K or V: a block of 64 elements
+  static constexpr int kBlockBytes = kBoxes * kBox;
+  static constexpr int kHalves = kKeys / 64;                      // a thread has one row and 64 keys
+  static constexpr int kEw = 4 * kHalves;                         // elementwise warps; behind them MMA, TMA, scrubbing, idle
+  static constexpr int kThreads = 32 * (kEw + 4);
+  static constexpr int kCtas = HD == 128 ? 1 : 2;                 // per SM
+  static constexpr int kTmem = 512 / kCtas;                       // columns: S | dP | dQ | dS of even blocks | of odd blocks
   // A K block is held until the product with dS, one block longer than its V block.
-  static constexpr int kK = HD == 128 ? 3 : 4;
-  static constexpr int kV = HD == 128 ? 2 : 3;
+  static constexpr int kK = HD == 128 ? 3 : 5;
+  static constexpr int kV = HD == 128 ? 2 : 4;
   static constexpr int kSlots = kK + kV;
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + 2 * KA_TILE * 4 + 512;
+  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kBlockBytes + 2 * KA_TILE * 4 + 512;
   static __device__ __forceinline__ int k_slot(int j) { return j % kK; }
   static __device__ __forceinline__ int v_slot(int j) { return kK + j % kV; }
 };
 
-// One CTA: 128 queries of one head.  Tensor memory: S | dP | dQ | dS of even blocks | of odd blocks.
-// All 8 elementwise warps work on one block at a time (a thread has one row and 64 of the 128 keys);
-// they copy S and dP to registers and free them at once, so that the next block's two products run
-// meanwhile, and the product with K follows when dS is written.
+// One CTA: 128 queries of one head.  All elementwise warps work on one block at a time; they copy S and dP to
+// registers and free them at once, so that the next block's two products run meanwhile, and the product with
+// K follows when dS is written.  Of dh <= 64, two CTAs of half the size share an SM (blocks of 64 keys, half
+// of the tensor memory): one's start, end and waits are hidden by the other (packed sequences of 5 to 2048 tokens, 32 heads: 81 us to 68).
+//
+// Where the tile sees 128 keys at most, the sum of p dP over them is D without the rounding of the stored
+// output, whose share of the error is largest in such rows (dq of 5 to 2048 tokens off by 0.0025 relative
+// without this, 0.0024 with; the rounding of dq itself is 0.0017).  A pass over the blocks ahead of the others
+// finds it.
 template <int HD>
-__global__ void __launch_bounds__(KB2_THREADS, 1)
+__global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ BwdAttnParams prm) {
@@ -65,18 +78,18 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   uint8_t* sQ = smem;
   uint8_t* sG = smem + Cfg::kTileBytes;
   uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
-  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kTileBytes);  // [2][128]
+  float* sD = reinterpret_cast<float*>(sRing + Cfg::kSlots * Cfg::kBlockBytes);  // [2][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(sD + 2 * KA_TILE);
   uint64_t* q_full = bars;
   uint64_t* full = q_full + 1;             // [slots]
   uint64_t* empty = full + Cfg::kSlots;    // [slots]
   uint64_t* sd_full = empty + Cfg::kSlots;
-  uint64_t* sd_free = sd_full + 1;         // 8 warps
-  uint64_t* ds_full = sd_free + 1;         // 8 warps
+  uint64_t* sd_free = sd_full + 1;         // elementwise warps
+  uint64_t* ds_full = sd_free + 1;         // elementwise warps
   uint64_t* k_raw = ds_full + 1;           // the last key block has arrived, to be scrubbed
   uint64_t* scrubbed = k_raw + 1;
   uint64_t* dq_done = scrubbed + 1;
-  uint64_t* d_full = dq_done + 1;          // 8 warps
+  uint64_t* d_full = dq_done + 1;          // elementwise warps
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(d_full + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -92,8 +105,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   const int kvh = head / prm.group;
   const AttnJob job = prm.jobs.far ? prm.jobs.far[ji] : prm.jobs.near[ji];
   const int m_seen = max(job.first + job.rows - 1, 0);
-  const int n_blk = (m_seen + KA_TILE - 1) / KA_TILE;
-  const bool ragged = (m_seen & (KA_TILE - 1)) != 0;  // the last block reaches past the sequence's keys
+  const int n_blk = (m_seen + Cfg::kKeys - 1) / Cfg::kKeys;
+  const int n_pre = m_seen <= KA_TILE ? n_blk : 0;        // blocks of the pass for D
+  const int n_all = n_pre + n_blk;
+  const bool ragged = (m_seen & (Cfg::kKeys - 1)) != 0;  // the last block reaches past the sequence's keys
 
   // The TMA warp sets up the barriers and sends the first loads off before the block meets; the elementwise
   // warps' loads for D go out before that, too.
@@ -102,28 +117,28 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const int j = i >> 1;
     const int slot = (i & 1) ? Cfg::v_slot(j) : Cfg::k_slot(j);
     uint64_t* bar = &full[slot];
-    if (ragged && i == 2 * (n_blk - 1)) {
+    if (ragged && i == 2 * (n_all - 1)) {
       bar = k_raw;
       mbar_arrive(&full[slot]);
     }
-    mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+    mbar_arrive_expect_tx(bar, Cfg::kBlockBytes);
     for (int b = 0; b < Cfg::kBoxes; ++b)
-      tma_load_4d(sRing + slot * Cfg::kTileBytes + b * KA_BOX_BYTES, (i & 1) ? &tmV : &tmK, bar, 64 * b, kvh,
-                  job.k0 + j * KA_TILE, rank, pol_kv);
+      tma_load_4d(sRing + slot * Cfg::kBlockBytes + b * Cfg::kBox, (i & 1) ? &tmV : &tmK, bar, 64 * b, kvh,
+                  job.k0 + (j < n_pre ? j : j - n_pre) * Cfg::kKeys, rank, pol_kv);
   };
-  if (threadIdx.x == 9 * 32) {
+  if (warp == Cfg::kEw + 1 && lane == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < Cfg::kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     mbar_init(sd_full, 1);
-    mbar_init(sd_free, 8);
-    mbar_init(ds_full, 8);
+    mbar_init(sd_free, Cfg::kEw);
+    mbar_init(ds_full, Cfg::kEw);
     mbar_init(k_raw, 1);
     mbar_init(scrubbed, 1);
     mbar_init(dq_done, 1);
-    mbar_init(d_full, 8);
+    mbar_init(d_full, Cfg::kEw);
     fence_mbar_init();
     if (n_blk > 0) {
       mbar_arrive_expect_tx(q_full, 2 * Cfg::kTileBytes);
@@ -133,39 +148,37 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       load_kv(1);
     }
   }
-  // Where one block holds all keys that the tile sees, the sum of p dP over it is D without the rounding of
-  // the stored output, whose share of the error is largest in such rows (dq of 5 to 2048 tokens off by
-  // 0.0025 relative without this, 0.0024 with; the rounding of dq itself is 0.0017).
-  const bool one = n_blk == 1;
-  uint4 d_o[8], d_g[8];  // 16 lanes a row, a warp 16 rows
-  if (warp < 8 && !one) {
-    const int e = 8 * (lane & 15);
+  constexpr int kLanes = HD / 8;  // of a row, for D; a warp's rows: 8 times as many as it has at once
+  uint4 d_o[8], d_g[8];
+  if (warp < Cfg::kEw && n_pre == 0) {
+    const int e = 8 * (lane % kLanes);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 16 * warp + 2 * i + (lane >> 4);
+      const int r = (8 * warp + i) * (32 / kLanes) + lane / kLanes;
       const bool in = r < job.rows && e < prm.dh;
       const int64_t off = ((rank * prm.Tq + job.q0 + r) * prm.hq + head) * prm.dh + e;
       d_o[i] = in ? ld_nc_v4(prm.out + off) : make_uint4(0, 0, 0, 0);
       d_g[i] = in ? ld_nc_v4(prm.dout + off) : make_uint4(0, 0, 0, 0);
     }
   }
-  if (warp == 8) {
-    tmem_alloc(tmem_holder, 512);
+  if (warp == Cfg::kEw) {
+    tmem_alloc(tmem_holder, Cfg::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
+  const uint32_t tmem = Cfg::kCtas == 1 ? 0 : *tmem_holder;  // all 512 columns: the allocation starts at the first
   const uint64_t tmo = prm.timeout_ns;
-  constexpr uint32_t kDP = KA_TILE, kDQ = 2 * KA_TILE, kDS = 3 * KA_TILE;  // tensor memory columns
+  constexpr uint32_t kDP = Cfg::kKeys, kDQ = 2 * Cfg::kKeys, kDS = kDQ + HD;  // tensor memory columns
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 9) {
+  if (warp >= Cfg::kEw) {
+    if constexpr (HD == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == Cfg::kEw + 1) {
       if (lane == 0 && n_blk > 0) {
         bool ok = true;
-        for (int i = 2; i < 2 * n_blk && ok; ++i) {
+        for (int i = 2; i < 2 * n_all && ok; ++i) {
           const int j = i >> 1;
           const int slot = (i & 1) ? Cfg::v_slot(j) : Cfg::k_slot(j);
           ok = mbar_wait(&empty[slot], ((j / ((i & 1) ? Cfg::kV : Cfg::kK)) & 1) ^ 1, tmo, 111);
@@ -173,31 +186,31 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         }
         if (!ok) spin_ns(KA_DRAIN_NS);
       }
-    } else if (warp == 8) {
+    } else if (warp == Cfg::kEw) {
       if (n_blk > 0) {
         const uint32_t lead = elect_one();
-        constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KA_TILE);
+        constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, Cfg::kKeys);
         constexpr uint32_t id_q = idesc_bf16_f32_major(KA_TILE, HD, false, true);
-        constexpr uint32_t kTile16 = Cfg::kTileBytes >> 4;
+        constexpr uint32_t kBlock16 = Cfg::kBlockBytes >> 4;
         const uint64_t dQ = sw128_kmajor_desc(smem_u32(sQ)), dG = sw128_kmajor_desc(smem_u32(sG));
         const uint64_t dR = sw128_kmajor_desc(smem_u32(sRing)), dRt = sw128_mnmajor_desc_128(smem_u32(sRing));
         int ks = 0, vs = 0;            // slots of the next K and V block, and their phases
         uint32_t kp = 0, vp = 0;
         auto scores = [&](int j) {
           if (!lane_wait(&full[ks], kp, tmo, 112)) return false;
-          if (ragged && j == n_blk - 1 && !lane_wait(scrubbed, 0, tmo, 113)) return false;
-          const uint64_t dk = dR + ks * kTile16;
+          if (ragged && j == n_all - 1 && !lane_wait(scrubbed, 0, tmo, 113)) return false;
+          const uint64_t dk = dR + ks * kBlock16;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4;
-            umma_ss(lead, tmem, dQ + off, dk + off, id_s, kk > 0);
+            umma_ss(lead, tmem, dQ + off, dk + (((kk >> 2) * Cfg::kBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
           }
           if (!lane_wait(&full[Cfg::kK + vs], vp, tmo, 114)) return false;
-          const uint64_t dv = dR + (Cfg::kK + vs) * kTile16;
+          const uint64_t dv = dR + (Cfg::kK + vs) * kBlock16;
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * KA_BOX_BYTES + (kk & 3) * 32) >> 4;
-            umma_ss(lead, tmem + kDP, dG + off, dv + off, id_s, kk > 0);
+            umma_ss(lead, tmem + kDP, dG + off, dv + (((kk >> 2) * Cfg::kBox + (kk & 3) * 32) >> 4), id_s, kk > 0);
           }
           // also the completion of the product with dS two blocks back, whose buffer comes next
           umma_arrive(lead, sd_full);
@@ -208,42 +221,46 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         };
         bool ok = lane_wait(q_full, 0, tmo, 115) && scores(0);
         int kq = 0;  // slot of the block whose dS comes next
-        for (int j = 0; j < n_blk && ok; ++j) {
-          if (j + 1 < n_blk) {
+        for (int j = 0; j < n_all && ok; ++j) {
+          if (j + 1 < n_all) {
             ok = lane_wait(sd_free, j & 1, tmo, 116);
             if (!ok) break;
             tc_fence_after();
             ok = scores(j + 1);
             if (!ok) break;
           }
-          ok = lane_wait(ds_full, j & 1, tmo, 117);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t dk = dRt + kq * kTile16;
+          if (j >= n_pre) {
+            const int i = j - n_pre;
+            ok = lane_wait(ds_full, i & 1, tmo, 117);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t dk = dRt + kq * kBlock16;
 #pragma unroll
-          for (int kk = 0; kk < KA_TILE / 16; ++kk)
-            umma_ts(lead, tmem + kDQ, tmem + kDS + (j & 1) * 64 + 8 * kk, dk + (kk * 2048 >> 4), id_q,
-                    (j > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < Cfg::kKeys / 16; ++kk)
+              umma_ts(lead, tmem + kDQ, tmem + kDS + (i & 1) * (Cfg::kKeys / 2) + 8 * kk, dk + (kk * 2048 >> 4), id_q,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+          }
           umma_arrive(lead, &empty[kq]);
           if (++kq == Cfg::kK) kq = 0;
         }
         umma_arrive(lead, dq_done);
         lane_wait(dq_done, 0, tmo, 118);
       }
-    } else if (warp == 10 && ragged) {
+    } else if (warp == Cfg::kEw + 2 && ragged) {
       if (warp_wait(k_raw, 0, tmo, 119)) {
-        uint8_t* k = sRing + Cfg::k_slot(n_blk - 1) * Cfg::kTileBytes;
-        const int live = m_seen - (n_blk - 1) * KA_TILE;
+        uint8_t* k = sRing + Cfg::k_slot(n_all - 1) * Cfg::kBlockBytes;
+        const int live = m_seen - (n_blk - 1) * Cfg::kKeys;
         for (int b = 0; b < Cfg::kBoxes; ++b)
-          for (int x = live * 8 + lane; x < KA_TILE * 8; x += 32)
-            reinterpret_cast<uint4*>(k + b * KA_BOX_BYTES)[x] = make_uint4(0, 0, 0, 0);
+          for (int x = live * 8 + lane; x < Cfg::kKeys * 8; x += 32)
+            reinterpret_cast<uint4*>(k + b * Cfg::kBox)[x] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(scrubbed);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    if constexpr (HD == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int w = warp >> 2;  // which half of the block's keys, and of dQ's columns at the end
     const int q = warp & 3;
     const int row = q * 32 + lane;
@@ -252,8 +269,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const int64_t grow = job.q0 + row;
     const int64_t srow = (int64_t(rank) * prm.hq + head) * prm.Tq + grow;
     float D = 0.f;
-    if (!one) {
-      // D: a row a lane, the loads touched 32 rows each and took 12,000 clocks
+    if (n_pre == 0) {
+      // (a row a lane, the loads touched 32 rows each and took 12,000 clocks)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t wa[4] = {d_o[i].x, d_o[i].y, d_o[i].z, d_o[i].w}, wb[4] = {d_g[i].x, d_g[i].y, d_g[i].z, d_g[i].w};
@@ -264,10 +281,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
           part = fmaf(bf16hi(wa[u]), bf16hi(wb[u]), part);
         }
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
-        if ((lane & 15) == 0) sD[16 * warp + 2 * i + (lane >> 4)] = part;
+        for (int e = kLanes / 2; e > 0; e >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, e);
+        if (lane % kLanes == 0) sD[(8 * warp + i) * (32 / kLanes) + lane / kLanes] = part;
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::kEw) : "memory");
       D = sD[row];
       if (mine && w == 0) prm.D[srow] = D;
     }
@@ -277,7 +294,8 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     const uint64_t c2 = pack_f32x2(c, c), nl2 = pack_f32x2(nl, nl);
     const int vis = job.first + row;
     bool ok = true;
-    for (int j = 0; j < n_blk; ++j) {
+    uint64_t sum2 = 0;
+    for (int j = 0; j < n_all; ++j) {
       ok = warp_wait(sd_full, j & 1, tmo, 120);
       if (!ok) break;
       tc_fence_after();
@@ -292,8 +310,9 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sd_free);
-      const int seen = vis - j * KA_TILE - 64 * w;
-      const bool cut = job.first + q * 32 - j * KA_TILE - 64 * w < 64;
+      const int key0 = (j < n_pre ? j : j - n_pre) * Cfg::kKeys + 64 * w;
+      const int seen = vis - key0;
+      const bool cut = job.first + q * 32 - key0 < 64;
       if (cut) {
         // unseen: s = -inf makes p = 0, and dP = 0 keeps dS = p (dP - D) from being 0 times a NaN
 #pragma unroll
@@ -308,19 +327,23 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         return pack_f32x2(ex2(a), ex2(b));
       };
       auto dp = [&](int y) { return pack_f32x2(__uint_as_float(g[2 * y]), __uint_as_float(g[2 * y + 1])); };
-      if (one) {
-        uint64_t sum2 = 0;
-        float a, b;
+      if (j < n_pre) {
 #pragma unroll
         for (int y = 0; y < 32; ++y) sum2 = fma_f32x2(prob(y), dp(y), sum2);
+        if (j + 1 < n_pre) continue;
+        float a, b;
         unpack_f32x2(sum2, a, b);
-        sD[w * KA_TILE + row] = a + b;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(d_full);
-        ok = warp_wait(d_full, 0, tmo, 122);
-        if (!ok) break;
-        D = sD[row] + sD[KA_TILE + row];
+        D = a + b;
+        if constexpr (Cfg::kHalves == 2) {
+          sD[w * KA_TILE + row] = D;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(d_full);
+          ok = warp_wait(d_full, 0, tmo, 122);
+          if (!ok) break;
+          D = sD[row] + sD[KA_TILE + row];
+        }
         if (mine && w == 0) prm.D[srow] = D;
+        continue;
       }
       const uint64_t nd2 = pack_f32x2(-D, -D);
       uint32_t p[32];
@@ -330,7 +353,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         unpack_f32x2(mul_f32x2(prob(y), add_f32x2(dp(y), nd2)), x0, x1);
         p[y] = pack_bf16x2(x0, x1);
       }
-      tmem_st_32x32b_x32(lanes + kDS + (j & 1) * 64 + 32 * w, p);
+      tmem_st_32x32b_x32(lanes + kDS + ((j - n_pre) & 1) * (Cfg::kKeys / 2) + 32 * w, p);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -340,10 +363,10 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     tc_fence_after();
     if (ok) {
       // every product is done: the Q tile's place serves to turn the rows
-      const int e = w * (HD / 2);
-      uint4 v[HD / 16];
+      const int e = 64 * w;
+      uint4 v[8];
 #pragma unroll
-      for (int x = 0; x < HD / 2; x += 32) {
+      for (int x = 0; x < 64; x += 32) {
         uint32_t o[32];
         if (n_blk > 0) {
           tmem_ld_32x32b_x32(lanes + kDQ + e + x, o);
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         }
       }
       const int64_t base = ((rank * prm.Tq + job.q0 + q * 32) * prm.hq + head) * prm.dh + e;
-      warp_store_rows(sQ + warp * (32 * HD), v, reinterpret_cast<uint8_t*>(prm.dq + base), int64_t(prm.hq) * prm.dh * 2,
+      warp_store_rows(sQ + warp * 4096, v, reinterpret_cast<uint8_t*>(prm.dq + base), int64_t(prm.hq) * prm.dh * 2,
                       job.rows - q * 32, (prm.dh - e) / 8, lane);
     }
   }
@@ -367,7 +390,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == Cfg::kEw) tmem_dealloc(tmem, Cfg::kTmem);
 }
 
 template <int HD>
