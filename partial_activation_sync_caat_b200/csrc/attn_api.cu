@@ -235,10 +235,12 @@ caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, co
   const int group = a->heads_q / a->heads_k;
   static thread_local std::vector<caat::AttnJob> jobs;
   static thread_local caat::FwdParams prm;
-  // Two heads of a group on the same 128 rows when the group is even: both tiles then need the same
-  // key blocks, and a short sequence wastes less than with 256 rows of one head.
-  prm.pair_heads = group % 2 == 0 ? 1 : 0;
-  query_jobs(a->cu_q, cu_k, a->n_seq, prm.pair_heads ? caat::KA_TILE : 2 * caat::KA_TILE, jobs);
+  // A CTA has one tile (dh <= 64), or two.  Two heads of a group on the same 128 rows when the group is
+  // even: both tiles then need the same key blocks, and a short sequence wastes less than with 256 rows of
+  // one head.
+  const bool two = a->dh > 64;
+  prm.pair_heads = two && group % 2 == 0 ? 1 : 0;
+  query_jobs(a->cu_q, cu_k, a->n_seq, two && !prm.pair_heads ? 2 * caat::KA_TILE : caat::KA_TILE, jobs);
   if (jobs.empty()) return CAAT_OK;
   prm.out = reinterpret_cast<__nv_bfloat16*>(a->out);
   prm.lse = a->lse;
@@ -255,7 +257,7 @@ caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, co
   const int64_t units = int64_t(jobs.size()) * a->P * n_heads;
   if (units > INT32_MAX) return CAAT_ERR_UNSUPPORTED;
   prm.n_units = static_cast<int>(units);
-  const int64_t grid = std::min<int64_t>(units, sms);
+  const int64_t grid = std::min<int64_t>(units, (two ? caat::FwdCfg<128>::kCtas : caat::FwdCfg<64>::kCtas) * int64_t(sms));
   CUtensorMap mq, mk, mv;
   if ((s = heads_map(&mq, q, a->P, a->Tq, a->heads_q, a->dh)) != CAAT_OK) return s;
   // no keys at all: every row is empty and neither map is used
@@ -265,9 +267,9 @@ caat_status launch_attn_forward(const caat_attn_args* a, const int32_t* cu_k, co
   Recorder rec;
   rec.begin(a->timing, a->stream);
   if (a->dh <= 64)
-    caat::attn_fwd_kernel<64><<<static_cast<unsigned>(grid), caat::KF_THREADS, caat::FwdCfg<64>::kSmem, a->stream>>>(mq, mk, mv, prm);
+    caat::attn_fwd_kernel<64><<<static_cast<unsigned>(grid), caat::FwdCfg<64>::kThreads, caat::FwdCfg<64>::kSmem, a->stream>>>(mq, mk, mv, prm);
   else
-    caat::attn_fwd_kernel<128><<<static_cast<unsigned>(grid), caat::KF_THREADS, caat::FwdCfg<128>::kSmem, a->stream>>>(mq, mk, mv, prm);
+    caat::attn_fwd_kernel<128><<<static_cast<unsigned>(grid), caat::FwdCfg<128>::kThreads, caat::FwdCfg<128>::kSmem, a->stream>>>(mq, mk, mv, prm);
   if (cudaGetLastError() != cudaSuccess) return CAAT_ERR_CUDA;
   rec.after_kernel(a->stream);
   return CAAT_OK;

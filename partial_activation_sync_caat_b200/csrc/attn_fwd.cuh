@@ -35,7 +35,6 @@
 
 namespace caat {
 
-constexpr int KF_THREADS = 384;
 // Every 8th pair of exponentials comes from a polynomial on the FMA units: the special-function units
 // (16 per clock and SM) bound a step.  T=8192, 32 heads: none 482 us, every 8th 462-472, every 4th 464-474.
 constexpr int KF_POLY = 8;
@@ -46,8 +45,13 @@ template <int HD>
 struct FwdCfg {
   static constexpr int kBoxes = HD / 64;
   static constexpr int kTileBytes = kBoxes * KA_BOX_BYTES;      // one Q, K or V tile
-  static constexpr int kSlots = HD == 128 ? 5 : 10;             // ring of K and V tiles
-  static constexpr int kSmem = 1024 + 2 * kTileBytes + kSlots * kTileBytes + 2 * HD * 4 + 512;
+  static constexpr int kTiles = HD == 128 ? 2 : 1;              // of queries
+  static constexpr int kCtas = 3 - kTiles;                      // per SM
+  static constexpr int kSlots = HD == 128 ? 5 : 6;              // ring of K and V tiles
+  static constexpr int kSoft = 4 * kTiles;                      // softmax warps; behind them MMA, K and V, Q and scrubbing, MMA
+  static constexpr int kThreads = 32 * (kSoft + 4);
+  static constexpr int kTmem = 512 / kCtas;                     // columns
+  static constexpr int kSmem = kTiles * kTileBytes + kSlots * kTileBytes + 2 * HD * 4 + 512;
 };
 
 struct FwdParams {
@@ -124,13 +128,13 @@ struct FwdUnit {
 };
 
 template <int HD>
-__global__ void __launch_bounds__(KF_THREADS, 1)
+__global__ void __launch_bounds__(FwdCfg<HD>::kThreads, FwdCfg<HD>::kCtas)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdParams prm) {
   using Cfg = FwdCfg<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];  // (a known address: no registers spent on it)
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + 2 * Cfg::kTileBytes;
+  uint8_t* sRing = smem + Cfg::kTiles * Cfg::kTileBytes;
   // [2][HD], by the unit's parity: the first key (from block j_odd on) whose value is NaN, +inf, -inf,
   // 10 bits each, 1023: none
   uint32_t* odd = reinterpret_cast<uint32_t*>(sRing + Cfg::kSlots * Cfg::kTileBytes);
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
   uint64_t* v_full = o_free + 2;             // [KF_ODD] V blocks to scrub have arrived
   uint64_t* scrubbed = v_full + KF_ODD;      // [KF_ODD]
   uint64_t* scrub_done = scrubbed + KF_ODD;  // [2] all of a unit's
-  uint64_t* epi_done = scrub_done + 2;       // [2] 8 warps
+  uint64_t* epi_done = scrub_done + 2;       // [2] softmax warps
   uint64_t* mma_done = epi_done + 2;
   volatile int* any_odd = reinterpret_cast<int*>(mma_done + 1);  // [2]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 2);
@@ -170,37 +174,40 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
       }
       mbar_init(&o_free[t], 4);
       mbar_init(&scrub_done[t], 1);
-      mbar_init(&epi_done[t], 8);
+      mbar_init(&epi_done[t], Cfg::kSoft);
       any_odd[t] = 0;
     }
     for (int s = 0; s < Cfg::kSlots; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);
+      mbar_init(&empty[s], Cfg::kTiles);
     }
     for (int s = 0; s < KF_ODD; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&scrubbed[s], 1);
     }
-    mbar_init(mma_done, 2);
+    mbar_init(mma_done, Cfg::kTiles);
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  for (int i = threadIdx.x; i < 2 * HD; i += KF_THREADS) odd[i] = 0x3FFFFFFFu;
-  if (warp == 8) {
-    tmem_alloc(tmem_holder, 512);
+  for (int i = threadIdx.x; i < 2 * HD; i += Cfg::kThreads) odd[i] = 0x3FFFFFFFu;
+  const int role = warp - Cfg::kSoft;
+  if (role == 0) {
+    tmem_alloc(tmem_holder, Cfg::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  constexpr uint32_t tmem = 0;  // all 512 columns: the allocation starts at the first
+  const uint32_t tmem = Cfg::kCtas == 1 ? 0 : *tmem_holder;  // all 512 columns: the allocation starts at the first
+  constexpr uint32_t kO = Cfg::kTiles * KA_TILE;
   const uint64_t tmo = prm.timeout_ns;
   FwdUnit u;
 
-  if (warp >= 8) {
-    if (warp == 9) {
+  if (role >= 0) {
+    if constexpr (Cfg::kCtas == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (role == 1) {
       // -------------------------------------------------------------- TMA: K and V
       if (lane == 0) {
         const uint64_t pol_kv = policy_evict_last();
@@ -226,9 +233,9 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
         }
         if (!ok && issued) spin_ns(KA_DRAIN_NS);
       }
-    } else if (warp != 10) {
-      // -------------------------------------------------------------- MMA: warp 8 of tile 0, 11 of tile 1
-      const int t = warp == 8 ? 0 : 1;
+    } else if (role != 2) {
+      // -------------------------------------------------------------- MMA: the first of tile 0, the last of tile 1
+      const int t = Cfg::kTiles == 1 || role == 0 ? 0 : 1;
       const uint32_t lead = elect_one();
       constexpr uint32_t id_s = idesc_bf16_f32(KA_TILE, KF_STEP);
       constexpr uint32_t id_o = idesc_bf16_f32_major(KA_TILE, HD, false, true);
@@ -256,7 +263,8 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
         umma_arrive(lead, &s_full[2 * t + buf]);
       };
       FwdSpan u;
-      bool ok = true;
+      const bool idle = Cfg::kTiles == 1 && role != 0;
+      bool ok = !idle;
       for (int k = 0; ok && u.get(prm, k); ++k) {
         if (u.n_blk == 0) continue;
         const int nb = t ? u.nb[1] : u.nb[0];
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
             const uint64_t b = dV + static_cast<uint32_t>(v * (Cfg::kTileBytes >> 4) + h * (KF_STEP * 128 >> 4));
 #pragma unroll
             for (int kk = 0; kk < KF_STEP / 16; ++kk)
-              umma_ts(lead, tmem + 2 * KA_TILE + t * HD, tmem + t * KA_TILE + buf * KF_STEP + 8 * kk, b + (kk * 2048 >> 4), id_o,
+              umma_ts(lead, tmem + kO + t * HD, tmem + t * KA_TILE + buf * KF_STEP + 8 * kk, b + (kk * 2048 >> 4), id_o,
                       (j > 0 || kk > 0) ? 1u : 0u);
             umma_arrive(lead, &pv_done[2 * t + buf]);
             ++np;
@@ -309,8 +317,10 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
           if (more) umma_arrive(lead, &empty[kn]);
         }
       }
-      umma_arrive(lead, mma_done);
-      lane_wait(mma_done, 0, tmo, 99);
+      if (!idle) {
+        umma_arrive(lead, mma_done);
+        lane_wait(mma_done, 0, tmo, 99);
+      }
     } else {
       // -------------------------------------------------------------- TMA of Q; scrubbing V
       const uint64_t pol_q = policy_evict_first();
@@ -405,12 +415,13 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
+    if constexpr (Cfg::kCtas == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int t = warp >> 2;
     const int q = warp & 3;
     const int row = q * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t tS0 = tmem + lane_base + t * KA_TILE;
-    const uint32_t tO = tmem + lane_base + 2 * KA_TILE + t * HD;
+    const uint32_t tO = tmem + lane_base + kO + t * HD;
     const float c = prm.scale * KA_LOG2E;
     const uint64_t c2 = pack_f32x2(c, c);
     bool ok = true;
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(KF_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (role == 0) tmem_dealloc(tmem, Cfg::kTmem);
 }
 
 }  // namespace caat
