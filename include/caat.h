@@ -548,7 +548,7 @@ CAAT_API caat_status caat_rope(const caat_rope_args* args);
  *   out        device bf16 [P, Tq, heads_q * dh] contiguous; must not overlap the inputs
  *   lse        device fp32 [P, heads_q, Tq], or NULL
  *   cu_q, cu_k HOST int32 [n_seq + 1], non-decreasing, from >= 0 up to <= Tq | Tk; cu_k NULL: cu_q.
- *              Read before return.
+ *              Read before return.  A sequence has at most 2^25 queries and keys.
  *   dh         dh % 8 == 0, dh <= 128;  heads_q % heads_k == 0;  scale > 0, finite
  *   workspace  caat_attn_workspace_size(..., CAAT_VARIANT_ATTN) bytes, 256-byte aligned; NULL when
  *              that is 0.  Clobbered.

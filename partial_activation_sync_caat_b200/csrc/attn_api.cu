@@ -44,6 +44,9 @@ using caat::host::Recorder;
 constexpr size_t kDecodeCounters = 2048;  // 4 bytes per CTA
 static_assert(caat::KD_CTAS * 4 <= kDecodeCounters, "one counter per CTA");
 constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a buffer, rows of a sequence's cache
+// A warp may wait through a whole sequence (for its last block, 64 keys each 1,000 to 2,000 clocks): within the
+// waits' limit of 2 s.
+constexpr int kMaxSequence = 1 << 25;
 constexpr int64_t kMaxCacheRows = int64_t(1) << 36;  // of all sequences: far more than fit the memory
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -97,7 +100,10 @@ caat_status check_offsets(const int32_t* cu, int n_seq, int64_t T) {
   if (cu[0] < 0) return CAAT_ERR_INVALID_ARG;
   for (int i = 0; i < n_seq; ++i)
     if (cu[i + 1] < cu[i]) return CAAT_ERR_INVALID_ARG;
-  return cu[n_seq] <= T ? CAAT_OK : CAAT_ERR_INVALID_ARG;
+  if (cu[n_seq] > T) return CAAT_ERR_INVALID_ARG;
+  for (int i = 0; i < n_seq; ++i)
+    if (cu[i + 1] - cu[i] > kMaxSequence) return CAAT_ERR_UNSUPPORTED;
+  return CAAT_OK;
 }
 
 // One-time kernel attributes, per device and context.

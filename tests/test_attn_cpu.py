@@ -161,6 +161,9 @@ def test_attention_refuses(L, name):
                dict(Tq=(1 << 30) + 1), dict(q_stride_token=516, q_stride_rank=516 * 300),
                dict(q_stride_token=(1 << 31) + 8, q_stride_rank=1 << 34)):
         assert attn(L, name, **kw) == C.CAAT_ERR_UNSUPPORTED, kw
+    long = np.array([0, 1 << 25, (1 << 26) + 1], dtype=np.int32)
+    big = dict(Tq=1 << 27, Tk=1 << 27, P=1, heads_q=1, heads_k=1, dh=8, k=1 << 40, v=1 << 41, out=1 << 42, lse=1 << 43)
+    assert attn(L, name, cu_q=long.ctypes.data, **big) == C.CAAT_ERR_UNSUPPORTED
     assert attn(L, name, n_seq=0, q=None) == C.CAAT_OK
     if name == "caat_attn_forward":
         assert attn(L, out=0x1000100) == C.CAAT_ERR_INVALID_ARG   # out inside q
