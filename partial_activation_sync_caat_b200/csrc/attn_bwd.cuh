@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
     if (threadIdx.x == 0) status_raise(2, 90);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ji = blockIdx.x / prm.per_job;
   const int rh = blockIdx.x - ji * prm.per_job;
   const int rank = rh / prm.hq;
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
     if (threadIdx.x == 0) status_raise(2, 90);
     return;
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int ji = blockIdx.x / prm.per_job;
   int rest = blockIdx.x - ji * prm.per_job;
   const int split = rest % prm.splits;
@@ -561,6 +563,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
         lane_wait(done, 0, tmo, 135);
       }
     } else if (warp == 10) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // D is there (and no CTA ends before the dq kernel)
       for (int i = 0; i < n; ++i) {
         const int st = i % Cfg::kStages;
         const uint32_t ph = (i / Cfg::kStages) & 1;
@@ -711,6 +714,7 @@ __global__ void __launch_bounds__(KB2_THREADS, 1)
 // 16-byte piece of dk or dv, four splits' loads in flight (packed 4096 tokens, 4 ranks of one key head of 64,
 // 3 splits, 25 MB: 9.3 to 10.2 us between events; with two pieces a thread, one after another, 11.1).
 __global__ void __launch_bounds__(256) attn_dkv_join_kernel(const __grid_constant__ BwdAttnParams prm) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttnJob job = prm.jobs.far ? prm.jobs.far[blockIdx.x] : prm.jobs.near[blockIdx.x];
   const int rank = blockIdx.y, w = blockIdx.z & 1;
   const int vecs = prm.hk * prm.dh / 4;  // a key's row over all heads
