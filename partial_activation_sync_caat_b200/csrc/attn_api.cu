@@ -208,13 +208,16 @@ BwdLayout bwd_layout(int64_t Tq, int64_t Tk, int n_seq, int P, int hq, int hk, i
 // parts of 2048 keys at most, so that a ragged batch's longest sequence ends with the others.  They start
 // slowly when more of them come than the SMs hold at once, which only parts of 1 MiB make up for (us,
 // clusters | even deal; dh 128: 32 segments of 2048 keys 8.6 | 15.5, of 8192 26.2 | 35.8; 512 of 256 keys
-// with 2 CTAs each 34.2 | 19.0, of 8192 with 4 301 | 331; 2048 of 256 keys, one CTA each, 47.9 | 54.4).
+// with 2 CTAs each 34.2 | 19.0, of 8192 with 4 301 | 331; 2048 of 256 keys, one CTA each, 47.9 | 54.4).  Few
+// segments leave SMs idle, which costs less than the deal's parts and second launch while a CTA has 16
+// tiles or fewer (dh 128: one segment of 600 keys 8.2 | 10.3, of 4096 10.3 | 14.3, of 8192 14.9 | 18.4;
+// 30 of 148 keys 8.2 | 16.6).
 int decode_cluster(int64_t B, int64_t capacity, int P, int hq, int hk, int dh) {
   const int64_t segs = B * P * hk * ((hq / hk + 15) / 16);
   const int tile = 4 * caat::kd_keys(dh <= 64 ? 64 : 128);
   int c = 1;
   while (c < 8 && (capacity > 2048 * c || (segs * c < 2 * 148 && 2 * c * tile <= capacity))) c *= 2;
-  if (capacity > 2048 * c || segs * c < 148 || segs * c > INT32_MAX) return 0;
+  if (capacity > 2048 * c || (segs * c < 148 && capacity > int64_t(16) * tile * c) || segs * c > INT32_MAX) return 0;
   return c == 1 || segs * c <= 4 * 148 || capacity / c * dh * 4 >= (1 << 20) ? c : 0;
 }
 

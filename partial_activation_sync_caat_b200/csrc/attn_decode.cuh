@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_kernel(const __grid
 
 // The same with a cluster of CTAs per segment instead of the even deal: each CTA takes an equal part of the
 // segment's tiles, and the parts are joined through distributed shared memory, so that there is one
-// launch and no workspace.  The deal is kept for what this does badly: fewer segments than fill the
-// SMs 8 CTAs apiece, and contexts so long that one sequence's part would outlast all others.
+// launch and no workspace.  The deal is kept for what this does badly: contexts so long that one
+// sequence's part would outlast all others, and short parts in more clusters than fit the SMs at once.
 template <int HD>
 __global__ void __launch_bounds__(KD_THREADS, 2) attn_decode_cluster_kernel(const __grid_constant__ DecodeAttnParams prm, int ctas) {
   extern __shared__ __align__(128) uint8_t smem_raw[];

@@ -192,7 +192,7 @@ def test_decode_refuses(L):
                dict(capacity=(1 << 30) + 1), dict(B=4096, capacity=1 << 30)):
         assert decode(L, **kw) == C.CAAT_ERR_UNSUPPORTED, kw
     for kw in (dict(workspace=None), dict(ws_bytes=1024), dict(workspace=0x6000010)):
-        assert decode(L, **kw) == C.CAAT_ERR_WORKSPACE, kw
+        assert decode(L, capacity=20000, **kw) == C.CAAT_ERR_WORKSPACE, kw
     assert decode(L, B=0, q=None) == C.CAAT_OK
 
 

@@ -23,6 +23,19 @@ def draw(seed, *shape):
     return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
 
 
+def slab(x, capacity):
+    """The cache with more rows behind, of NaN (or as it is)."""
+    if not capacity:
+        return x.cuda()
+    P, B, cap, hk, dh = x.shape
+    y = torch.full((P, B, capacity, hk, dh), float("nan"), dtype=x.dtype, device="cuda")
+    y[:, :, :cap] = x.cuda()
+    return y
+
+
+DEAL = 16500  # a capacity whose tiles are dealt to the CTAs; smaller ones have a cluster per segment
+
+
 def decode(q, kc, vc, lens, **kw):
     P, B, hq, dh = q.shape
     out = torch.full((P, B, hq * dh), 7.0, dtype=torch.bfloat16, device="cuda")
@@ -40,19 +53,27 @@ def decode(q, kc, vc, lens, **kw):
     # clusters of 8, 4, 2 and 1 CTAs per segment, of narrow and wide heads, more than 16 query heads to a key head
     (8, 4, 4, 64, 1500, [0, 1, 1500, 127, 129]), (8, 48, 2, 72, 700, [700, 1, 0, 350, 128, 64]),
     (16, 2, 2, 128, 130, [130, 64, 65, 1, 0, 129]), (16, 17, 1, 128, 60, [60, 0, 1, 33] * 4), (19, 1, 1, 128, 1024, [1024])])
-def test_matches_oracle(P, hq, hk, dh, cap, lens):
+@pytest.mark.parametrize("capacity", [None, DEAL])
+def test_matches_oracle(P, hq, hk, dh, cap, lens, capacity):
     B = len(lens)
     q, kc, vc = draw(1, P, B, hq, dh), draw(2, P, B, cap, hk, dh), draw(3, P, B, cap, hk, dh)
-    out = decode(q, kc, vc, lens)
+    need = C.caat_attn_workspace_size(B, capacity or cap, 0, P, hq, hk, dh, C.CAAT_VARIANT_ATTN_DECODE)
+    assert need > 0 or not capacity
+    out = decode(q, slab(kc, capacity), slab(vc, capacity), lens)
     assert C.caat_get_device_status() == 0
     check_out(out.cpu(), A.decode(q, kc, vc, lens))
 
 
 @pytest.mark.parametrize("P", [1, 20])
+@pytest.mark.parametrize("capacity", [140, DEAL])
 @pytest.mark.parametrize("junk", [float("nan"), float("inf")])
-def test_rows_behind_a_length_are_never_used(junk, P):
+def test_rows_behind_a_length_are_never_used(junk, capacity, P):
     lens = [70, 5, 128, 0]
-    q, kc, vc = draw(4, P, 4, 4, 64), draw(5, P, 4, 140, 2, 64), draw(6, P, 4, 140, 2, 64)
+    q = draw(4, P, 4, 4, 64)
+    kc, vc = slab(draw(5, P, 4, 140, 2, 64), capacity), slab(draw(6, P, 4, 140, 2, 64), capacity)
+    for b, n in enumerate(lens):
+        kc[:, b, n:] = 1
+        vc[:, b, n:] = 1
     a = decode(q, kc, vc, lens)
     for b, n in enumerate(lens):
         kc[:, b, n:] = junk
@@ -61,9 +82,10 @@ def test_rows_behind_a_length_are_never_used(junk, P):
 
 
 @pytest.mark.parametrize("P", [1, 60])
-def test_lengths_outside_the_cache_are_reported(P):
+@pytest.mark.parametrize("capacity", [10, DEAL])
+def test_lengths_outside_the_cache_are_reported(P, capacity):
     q, kc, vc = draw(7, P, 3, 2, 64), draw(8, P, 3, 10, 1, 64), draw(9, P, 3, 10, 1, 64)
-    out = decode(q, kc, vc, [11, 10, -1])
+    out = decode(q, slab(kc, capacity), slab(vc, capacity), [capacity + 1, 10, -1])
     assert C.caat_get_device_status() & 0xFF == C.CAAT_ERR_INVALID_ARG
     assert C.caat_get_device_status() == 0
     assert bool((out[:, [0, 2]] == 0).all())
@@ -71,14 +93,15 @@ def test_lengths_outside_the_cache_are_reported(P):
 
 
 @pytest.mark.parametrize("P", [2, 16])
-def test_same_bits_every_time_and_from_a_fused_projection(P):
+@pytest.mark.parametrize("capacity", [None, DEAL])
+def test_same_bits_every_time_and_from_a_fused_projection(P, capacity):
     """The parts of a cut sequence are joined in a fixed order, whichever CTA finishes last; q may be a
     slice of a fused projection."""
     B, hq, hk, dh, cap = 5, 8, 2, 64, 3000
     lens = [3000, 1, 777, 2999, 64]
     qkv = draw(30, P, B, (hq + 2 * hk) * dh).cuda()
     q = qkv[..., :hq * dh].unflatten(-1, (hq, dh))
-    kc, vc = draw(31, P, B, cap, hk, dh).cuda(), draw(32, P, B, cap, hk, dh).cuda()
+    kc, vc = slab(draw(31, P, B, cap, hk, dh), capacity), slab(draw(32, P, B, cap, hk, dh), capacity)
     first = decode(q.contiguous(), kc, vc, lens)
     for _ in range(10):
         assert torch.equal(first, decode(q, kc, vc, lens))
@@ -113,10 +136,10 @@ def test_large_scores():
     check_out(decode(q, kc, vc, [500, 300]).cpu(), A.decode(q, kc, vc, [500, 300]))
 
 
-@pytest.mark.parametrize("P", [2, 30])
-def test_captured_step_follows_the_lengths(P):
+@pytest.mark.parametrize("cap", [200, DEAL])
+def test_captured_step_follows_the_lengths(cap):
     """A captured step (append, decode) replayed over a growing context equals separate calls."""
-    B, hq, hk, dh, cap = 3, 4, 2, 64, 200
+    P, B, hq, hk, dh = 2, 3, 4, 2, 64
     freq, _ = C.caat_rope_frequencies(dh)
     kc, vc = draw(13, P, B, cap, hk, dh).cuda(), draw(14, P, B, cap, hk, dh).cuda()
     kc2, vc2 = kc.clone(), vc.clone()
@@ -125,7 +148,7 @@ def test_captured_step_follows_the_lengths(P):
     pos, slots, base = lens - 1, (lens - 1).long() + cap * torch.arange(B, device="cuda"), None
     out, qr = torch.empty(P, B, hq * dh, dtype=torch.bfloat16, device="cuda"), torch.empty_like(q)
     need = C.caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, C.CAAT_VARIANT_ATTN_DECODE)
-    assert (need == 0) == (P == 30)  # both kernels
+    assert (need == 0) == (cap == 200)  # both kernels
     ws = C.alloc_workspace(need)
 
     def step(kc, vc, out):

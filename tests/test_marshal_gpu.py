@@ -133,9 +133,9 @@ def test_workspace_of_the_call_and_of_the_caller(fused):
     with pytest.raises(C.CaatError) as e:
         C.caat_attn_forward(q, k, v, cu, outs[1], workspace=C.alloc_workspace(256)[:16])
     assert e.value.code == C.CAAT_ERR_WORKSPACE
-    cache = rand(1, 1, 5000, 1, DH), rand(1, 1, 5000, 1, DH)
+    cache = rand(1, 1, 20000, 1, DH), rand(1, 1, 20000, 1, DH)
     lens = torch.tensor([4999], device="cuda", dtype=torch.int32)
-    need = C.caat_attn_workspace_size(1, 5000, 0, 1, 2, 1, DH, C.CAAT_VARIANT_ATTN_DECODE)
+    need = C.caat_attn_workspace_size(1, 20000, 0, 1, 2, 1, DH, C.CAAT_VARIANT_ATTN_DECODE)
     assert need > 0
     outs = [rand(1, 1, 2 * DH) for _ in range(2)]
     C.caat_attn_decode(q[:, :1], *cache, lens, outs[0])
