@@ -77,6 +77,13 @@ CASES = [
     (8, 4, 4, 128, [300, 1, 129, 260], None),
     (4, 8, 2, 128, [140, 70, 257, 3, 128], [150, 70, 300, 2, 128]),
     (64, 1, 1, 16, [65, 64, 63], None),
+    # tiles that see 64, 65, 128 or 129 keys: where blocks, and the pass for D, end
+    (2, 2, 1, 64, [64, 65, 128, 129], None),
+    (2, 2, 1, 64, [100, 28, 1], [128, 129, 64]),
+    (1, 3, 1, 128, [100, 28, 129], [128, 129, 130]),
+    # a key tile's queries shared by CTAs
+    (1, 8, 1, 64, [1500], None),
+    (1, 4, 2, 96, [700, 20], [721, 20]),
 ]
 
 
