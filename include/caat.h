@@ -551,7 +551,7 @@ CAAT_API caat_status caat_rope(const caat_rope_args* args);
  *              Read before return.  A sequence has at most 2^25 queries and keys.
  *   dh         dh % 8 == 0, dh <= 128;  heads_q % heads_k == 0;  scale > 0, finite
  *   workspace  caat_attn_workspace_size(..., CAAT_VARIANT_ATTN) bytes, 256-byte aligned; NULL when
- *              that is 0.  Clobbered.
+ *              that is 0.  Clobbered; two calls that may overlap on the GPU need one each.
  * Capturable in a CUDA graph (which then holds the offsets of the captured call).
  */
 typedef struct caat_attn_args {
@@ -590,7 +590,7 @@ CAAT_API caat_status caat_attn_forward(const caat_attn_args* args);
  *   out, lse    the forward's results;  dout  device bf16 [P, Tq, heads_q * dh]
  *   dq [P, Tq, heads_q, dh], dk, dv [P, Tk, heads_k, dh]  device bf16, contiguous (out).  Keys that no
  *               query sees get zeros; rows outside every sequence are not written.
- *   workspace   caat_attn_workspace_size(..., CAAT_VARIANT_ATTN_BWD) bytes, 256-byte aligned
+ *   workspace   caat_attn_workspace_size(..., CAAT_VARIANT_ATTN_BWD) bytes, 256-byte aligned; as above
  * Outputs must not overlap the inputs or each other.  Values that are not finite make the gradients of
  * their own sequence unspecified; they never reach another sequence's.  Capturable as the forward.
  */
