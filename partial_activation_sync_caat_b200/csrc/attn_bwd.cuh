@@ -68,6 +68,12 @@ struct DqCfg {
 // output, whose share of the error is largest in such rows (dq of 5 to 2048 tokens off by 0.0025 relative
 // without this, 0.0024 with; the rounding of dq itself is 0.0017).  A pass over the blocks ahead of the others
 // finds it.
+//
+// dS has a barrier per buffer.  A warp frees S and dP before it has written its dS, so the next block's scores
+// may be there, and a fast warp be done with that block too, before a slow one has arrived for this: on one
+// barrier the fast warp's second arrival would count for the slow one's first, and the product would read 32 rows
+// that nobody has written.  A warp's next arrival on the same barrier, two blocks on, is behind the scores of
+// that block, which need every warp to have freed the block in between, and each does so after its arrival here.
 template <int HD>
 __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
@@ -85,8 +91,8 @@ __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
   uint64_t* empty = full + Cfg::kSlots;    // [slots]
   uint64_t* sd_full = empty + Cfg::kSlots;
   uint64_t* sd_free = sd_full + 1;         // elementwise warps
-  uint64_t* ds_full = sd_free + 1;         // elementwise warps
-  uint64_t* k_raw = ds_full + 1;           // the last key block has arrived, to be scrubbed
+  uint64_t* ds_full = sd_free + 1;         // [2 dS buffers] elementwise warps
+  uint64_t* k_raw = ds_full + 2;           // the last key block has arrived, to be scrubbed
   uint64_t* scrubbed = k_raw + 1;
   uint64_t* dq_done = scrubbed + 1;
   uint64_t* d_full = dq_done + 1;          // elementwise warps
@@ -135,7 +141,7 @@ __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
     }
     mbar_init(sd_full, 1);
     mbar_init(sd_free, Cfg::kEw);
-    mbar_init(ds_full, Cfg::kEw);
+    for (int b = 0; b < 2; ++b) mbar_init(&ds_full[b], Cfg::kEw);
     mbar_init(k_raw, 1);
     mbar_init(scrubbed, 1);
     mbar_init(dq_done, 1);
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
           }
           if (j >= n_pre) {
             const int i = j - n_pre;
-            ok = lane_wait(ds_full, i & 1, tmo, 117);
+            ok = lane_wait(&ds_full[i & 1], (i >> 1) & 1, tmo, 117);
             if (!ok) break;
             tc_fence_after();
             const uint64_t dk = dRt + kq * kBlock16;
@@ -354,11 +360,12 @@ __global__ void __launch_bounds__(DqCfg<HD>::kThreads, DqCfg<HD>::kCtas)
         unpack_f32x2(mul_f32x2(prob(y), add_f32x2(dp(y), nd2)), x0, x1);
         p[y] = pack_bf16x2(x0, x1);
       }
-      tmem_st_32x32b_x32(lanes + kDS + ((j - n_pre) & 1) * (Cfg::kKeys / 2) + 32 * w, p);
+      const int buf = (j - n_pre) & 1;
+      tmem_st_32x32b_x32(lanes + kDS + buf * (Cfg::kKeys / 2) + 32 * w, p);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full);
+      if (lane == 0) mbar_arrive(&ds_full[buf]);
     }
     if (ok && n_blk > 0) ok = warp_wait(dq_done, 0, tmo, 121);
     tc_fence_after();
