@@ -698,6 +698,8 @@ def _heads4(t, name, dtype, dev, shape=None):
         raise ValueError(f"{name}: the heads of a token must be contiguous and side by side")
     # a dimension of one element has no stride of its own
     token = s[1] if T > 1 else heads * dh
+    if token < heads * dh:  # (0, 0) would mean contiguous
+        raise ValueError(f"{name}: the tokens must not share memory")
     return t.data_ptr(), s[0] if P > 1 else max(s[0], token * T), token
 
 

@@ -55,7 +55,7 @@ bool like(PyObject* o, at::ScalarType type, c10::IntArrayRef shape, int dev, T**
 }
 
 // bf16 [P, T, heads, dh] whose heads lie side by side within a token: address and (rank, token) strides,
-// 0 for a contiguous tensor.
+// 0 for a contiguous tensor, and for no other.
 bool heads4(const at::Tensor* t, const caat_bf16** p, int64_t* rank, int64_t* token) {
   if (!t || t->dim() != 4 || t->scalar_type() != at::kBFloat16) return false;
   *p = static_cast<const caat_bf16*>(t->data_ptr());
@@ -64,6 +64,7 @@ bool heads4(const at::Tensor* t, const caat_bf16** p, int64_t* rank, int64_t* to
   const auto n = t->sizes(), s = t->strides();
   if ((n[3] > 1 && s[3] != 1) || (n[2] > 1 && s[2] != n[3])) return false;
   *token = n[1] > 1 ? s[1] : n[2] * n[3];  // a dimension of one element has no stride of its own
+  if (*token < n[2] * n[3]) return false;  // an expanded tensor: (0, 0) would mean contiguous
   *rank = n[0] > 1 ? s[0] : std::max(s[0], *token * n[1]);
   return true;
 }

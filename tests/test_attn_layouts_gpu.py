@@ -1,0 +1,59 @@
+"""Layouts of the attention block's tensors on the GPU: what is refused before any launch, and layouts of the
+ranks and tokens that other tests do not have."""
+import numpy as np
+import pytest
+import torch
+
+from partial_activation_sync_caat_b200 import caat as C
+
+from gpu_util import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ensure_built()
+
+
+@pytest.fixture(params=["compiled", "interpreted"])
+def marshalling(request, monkeypatch):
+    """Both halves of the binding."""
+    if request.param == "compiled":
+        assert C._fast() is not None
+    else:
+        monkeypatch.setattr(C, "_marshal", None)
+        monkeypatch.setattr(C, "_fast", lambda: None)
+
+
+@pytest.mark.parametrize("P,T", [(8, 16), (1, 16), (2, 2)])
+def test_expanded_tensors_are_refused(marshalling, P, T):
+    one = torch.ones(4, 64, dtype=BF, device="cuda")
+    wide = one.expand(P, T, 4, 64)
+    full = torch.zeros(P, T, 4, 64, dtype=BF, device="cuda")
+    out, lse = torch.zeros(P, T, 256, dtype=BF, device="cuda"), torch.zeros(P, 4, T, device="cuda")
+    freq, _ = C.caat_rope_frequencies(64)
+    cache = [torch.zeros(P, T, 4, 64, dtype=BF, device="cuda") for _ in range(2)]
+    slots = torch.arange(T, device="cuda")
+    grads = [torch.zeros_like(full) for _ in range(3)]
+    slab = torch.zeros(P, T, 8, 4, 64, dtype=BF, device="cuda")
+    lens = torch.ones(T, dtype=torch.int32, device="cuda")
+    calls = [lambda: C.caat_rope(wide, None, None, freq, q_out=wide, k_out=None),
+             lambda: C.caat_rope(wide, None, None, freq, q_out=full, k_out=None),
+             lambda: C.caat_rope(full, wide, None, freq, q_out=full, k_out=wide),
+             lambda: C.caat_rope_append(None, wide, full, None, slots, freq, *cache),
+             lambda: C.caat_rope_append(None, full, wide, None, slots, freq, *cache),
+             lambda: C.caat_attn_decode(wide, slab, slab, lens, out)]
+    for i in range(3):
+        qkv = [full, full, full]
+        qkv[i] = wide
+        calls.append(lambda qkv=qkv: C.caat_attn_forward(*qkv, [0, T], out))
+        calls.append(lambda qkv=qkv: C.caat_attn_backward(*qkv, out, lse, out, [0, T], *grads))
+    for call in calls:
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+    torch.cuda.synchronize()
+    assert bool((one == 1).all()) and not any(bool(x.any()) for x in (full, out, *cache, *grads))
+    assert C.caat_get_device_status() == 0
