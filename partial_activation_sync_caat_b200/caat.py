@@ -382,11 +382,16 @@ def caat_workspace_size(T: int, K: int, H: int, P: int, variant: int = CAAT_VARI
     return int(n)
 
 
-def alloc_workspace(nbytes: int, device=None):
-    """A device buffer for the workspace (allocated by torch, owned by the caller)."""
+def alloc_workspace(nbytes: int, device=None, stream=None):
+    """A device buffer for the workspace (allocated by torch, owned by the caller) of calls on `stream`
+    (None: the current one).  It comes from that stream's pool: one from another stream's may have just been
+    freed by work that is still queued there, and may be handed out again while the calls run."""
     import torch
     n = max(256, (int(nbytes) + 255) // 256 * 256)
-    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device="cuda" if device is None else device)
 
 
 # ---------------------------------------------------------------------------------------
@@ -406,7 +411,7 @@ def caat_rowpar_forward(X, W, residual, gamma, sync_idx, P: int, p: float, out, 
     K = int(X.shape[2]) * P
     H = int(W.shape[1])
     if workspace is None:
-        workspace = alloc_workspace(caat_workspace_size(T, K, H, P, CAAT_VARIANT_ROWPAR), X.device)
+        workspace = alloc_workspace(caat_workspace_size(T, K, H, P, CAAT_VARIANT_ROWPAR), X.device, stream)
     arr, idx_ptr = _sync_idx_host(sync_idx)
     a = RowparArgs()
     a.X = _bf16_dev(X, "X")
@@ -502,7 +507,7 @@ def caat_rowpar_tp_local(X, W, residual, p: float, zs, h, *, workspace=None, pri
     T, K_r = int(X.shape[0]), int(X.shape[1])
     H = int(W.shape[0])
     if workspace is None:
-        workspace = alloc_workspace(256, X.device)
+        workspace = alloc_workspace(256, X.device, stream)
     a = _tp_args(T, K_r, H, p, 1e-5, private_scale, stream, timing)
     a.X = _bf16_dev(X, "X")
     a.W = _bf16_dev(W, "W")
@@ -555,7 +560,7 @@ def caat_rowpar_tp_local_push(X, W, residual, p: float, h, peers: TpPeers, *, wo
     T, K_r = int(X.shape[0]), int(X.shape[1])
     H = int(W.shape[0])
     if workspace is None:
-        workspace = alloc_workspace(256, X.device)
+        workspace = alloc_workspace(256, X.device, stream)
     a = _tp_args(T, K_r, H, p, 1e-5, private_scale, stream, timing)
     a.X = _bf16_dev(X, "X")
     a.W = _bf16_dev(W, "W")
@@ -602,7 +607,7 @@ def caat_rowpar_backward(X, W, h, gamma, dout, sync_idx, P: int, p: float, dX, d
     K = int(X.shape[2]) * P
     H = int(W.shape[1])
     if workspace is None:
-        workspace = alloc_workspace(caat_workspace_size(T, K, H, P, CAAT_VARIANT_ROWPAR_BWD), X.device)
+        workspace = alloc_workspace(caat_workspace_size(T, K, H, P, CAAT_VARIANT_ROWPAR_BWD), X.device, stream)
     arr, idx_ptr = _sync_idx_host(sync_idx)
     a = BwdArgs()
     a.X, a.W, a.h = _bf16_dev(X, "X"), _bf16_dev(W, "W"), _bf16_dev(h, "h")
@@ -704,14 +709,11 @@ def _heads4(t, name, dtype, dev, shape=None):
 
 
 def _workspace(workspace, nbytes, dev, stream):
-    """(tensor or None, address, bytes) of a call's workspace; one allocated here is kept from
-    reuse until a stream other than the current one has finished with it."""
+    """(tensor or None, address, bytes) of a call's workspace; one allocated here belongs to the call's stream."""
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = alloc_workspace(nbytes)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = alloc_workspace(nbytes, dev, stream)
         return workspace, workspace.data_ptr(), nbytes
     if workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, not on device {dev}")
@@ -1046,7 +1048,7 @@ def caat_mlp_forward(X, A, W2, residual, gamma, sync_idx, P: int, p: float, out,
     H = int(X.shape[2])
     F = int(W2.shape[2]) * P
     if workspace is None:
-        workspace = alloc_workspace(caat_workspace_size(T, F, H, P, CAAT_VARIANT_MLP), X.device)
+        workspace = alloc_workspace(caat_workspace_size(T, F, H, P, CAAT_VARIANT_MLP), X.device, stream)
     arr, idx_ptr = _sync_idx_host(sync_idx)
     a = MlpArgs()
     a.X = _bf16_dev(X, "X")

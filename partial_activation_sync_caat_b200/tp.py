@@ -62,17 +62,18 @@ class TPRowParallel:
         h being the complete pre-norm residual stream of this rank."""
         import contextlib
         T = int(X_r.shape[0])
-        if zs is None or h is None:
-            zs, h = self.buffers(T, X_r.device)
         kw = {"private_scale": self.private_scale}
         if workspace is not None:
             kw["workspace"] = workspace
-        # the kernels and the collective are queued on the current stream (or `stream`)
+        # the kernels and the collective are queued on the current stream (or `stream`), whose pool the
+        # buffers come from, too
         ctx = contextlib.nullcontext()
         if stream is not None:
             import torch
             ctx = torch.cuda.stream(stream)
         with ctx:
+            if zs is None or h is None:
+                zs, h = self.buffers(T, X_r.device)
             self.local_fn(X_r, W_r, R_r, self.p, zs, h, **kw)
             if self.n_s > 0:
                 self.reduce_fn(zs)
