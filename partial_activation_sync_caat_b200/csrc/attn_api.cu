@@ -88,6 +88,20 @@ Range range_of(const void* p, size_t bytes) {
 bool meet(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 Range range_of(const View& v) { return {v.lo, v.hi}; }
 
+// Whether a row of `a` shares elements with one of `b`, two [P, T] tensors of rows of row_a and row_b elements with
+// the same strides, or with another row of `a` itself (b the same).  What counts is how far rows are apart: for
+// each difference in rank, the nearest row of `b` that ends behind the start of one of `a`.
+bool rows_meet(const View& a, int64_t row_a, const View& b, int64_t row_b, int P, int64_t T) {
+  const int64_t apart = (static_cast<int64_t>(b.lo) - static_cast<int64_t>(a.lo)) / 2;
+  for (int r = 1 - P; r < P; ++r) {
+    if (&a == &b && r == 0) continue;  // tokens of a rank are at least a row apart
+    const int64_t at = apart + r * a.rank, d = -row_b - at;  // b's row at at + t tok; the first t with t tok > d
+    const int64_t t = std::max((d >= 0 ? d / a.tok : -((-d + a.tok - 1) / a.tok)) + 1, 1 - T);
+    if (t < T && at + t * a.tok < row_a) return true;
+  }
+  return false;
+}
+
 caat_status check_heads(int P, int hq, int hk, int dh, float scale) {
   if (P < 1 || P > CAAT_MAX_P || hq < 1 || hk < 1 || dh < 1) return CAAT_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return CAAT_ERR_INVALID_ARG;
@@ -472,16 +486,15 @@ caat_status caat_rope(const caat_rope_args* a) {
   if (s != CAAT_OK) return s;
   for (int i = 0; i < n_in; ++i) {
     if (!written[i]) continue;
-    // in place: no row may lie on another one, of this tensor or of the others
+    // in place: no row may lie on another one, of this tensor or of the others (slices of one projection lie
+    // side by side within the same tokens)
     const View& w = read[i];
-    if (a->P > 1 && w.rank < (a->T - 1) * w.tok + row_of[i] && w.tok < (a->P - 1) * w.rank + row_of[i]) return CAAT_ERR_INVALID_ARG;
+    if (rows_meet(w, row_of[i], w, row_of[i], a->P, a->T)) return CAAT_ERR_INVALID_ARG;
     for (int j = 0; j < n_in; ++j) {
       if (j == i || !meet(in[i], in[j])) continue;
-      // slices of one projection: side by side within the same tokens
       const View& r = read[j];
-      if (w.tok != r.tok || (a->P > 1 && w.rank != r.rank)) return CAAT_ERR_INVALID_ARG;
-      const int64_t d = (r.p - w.p) % w.tok, ahead = d < 0 ? d + w.tok : d;
-      if (ahead < row_of[i] || ahead + row_of[j] > w.tok) return CAAT_ERR_INVALID_ARG;
+      if (w.tok != r.tok || (a->P > 1 && w.rank != r.rank) || rows_meet(w, row_of[i], r, row_of[j], a->P, a->T))
+        return CAAT_ERR_INVALID_ARG;
     }
     out[n_out++] = in[i];
   }

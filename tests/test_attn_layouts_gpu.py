@@ -57,3 +57,32 @@ def test_expanded_tensors_are_refused(marshalling, P, T):
     torch.cuda.synchronize()
     assert bool((one == 1).all()) and not any(bool(x.any()) for x in (full, out, *cache, *grads))
     assert C.caat_get_device_status() == 0
+
+
+def turned_alike(q, k, T, **kw):
+    """In place, against contiguous outputs: the same bits, and nothing else touched."""
+    freq, _ = C.caat_rope_frequencies(64)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") + 7
+    want = [torch.empty(x.shape, dtype=BF, device="cuda") for x in (q, k)]
+    C.caat_rope(q, k, pos, freq, q_out=want[0], k_out=want[1], **kw)
+    C.caat_rope(q, k, pos, freq, q_out=q, k_out=k, **kw)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    assert C.caat_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [2, 33])
+def test_rotated_in_place_ranks_inside_a_token(marshalling, T):
+    torch.manual_seed(T)
+    buf = torch.randn(T, 5, 2, 64, device="cuda").to(BF)
+    rest = buf[:, 4].clone()
+    turned_alike(buf[:, 0:2].transpose(0, 1), buf[:, 2:4].transpose(0, 1), T)
+    turned_alike(buf[:, 0:4:2].transpose(0, 1), buf[:, 1:4:2].transpose(0, 1), T, interleaved=True)
+    assert torch.equal(buf[:, 4], rest)
+    freq, _ = C.caat_rope_frequencies(64)
+    before = buf.clone()
+    with pytest.raises(C.CaatError) as e:  # k of rank 0 is q of rank 1
+        q, k = buf[:, 0:2].transpose(0, 1), buf[:, 1:3].transpose(0, 1)
+        C.caat_rope(q, k, None, freq, q_out=q, k_out=k)
+    assert e.value.code == C.CAAT_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before)
