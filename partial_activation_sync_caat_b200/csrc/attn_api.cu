@@ -493,7 +493,7 @@ caat_status caat_rope(const caat_rope_args* a) {
     for (int j = 0; j < n_in; ++j) {
       if (j == i || !meet(in[i], in[j])) continue;
       const View& r = read[j];
-      if (w.tok != r.tok || (a->P > 1 && w.rank != r.rank) || rows_meet(w, row_of[i], r, row_of[j], a->P, a->T))
+      if ((a->T > 1 && w.tok != r.tok) || (a->P > 1 && w.rank != r.rank) || rows_meet(w, row_of[i], r, row_of[j], a->P, a->T))
         return CAAT_ERR_INVALID_ARG;
     }
     out[n_out++] = in[i];

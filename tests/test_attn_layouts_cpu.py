@@ -111,3 +111,18 @@ def test_rotated_in_place_against_marked_elements(L, seed):
         assert code == (REFUSED if shared else ACCEPTED), (P, T, q, k)
         counts[code] += 1
     assert min(counts.values()) > 40
+
+
+def test_one_token_turned_in_place(L):
+    """A single token has no token stride: slices of one projection [P, 1, all] are apart by their rank stride,
+    whatever the call gives for the other one."""
+    hq, hk, dh, P = 4, 2, 64, 3
+    every, k0 = (hq + 2 * hk) * dh, hq * dh
+    for token_q, token_k in ((every, every), (hq * dh, hk * dh)):
+        q, k = (0, hq, every, token_q, True), (k0, hk, every, token_k, True)
+        assert turned(L, P, 1, q=q, k=k) == ACCEPTED
+        assert turned(L, P, 1, q=q, k=(*k[:4], False)) == ACCEPTED
+        assert turned(L, 1, 1, q=q, k=k) == ACCEPTED
+        assert turned(L, P, 1, q=q, k=(k0 - 8, hk, every, token_k, True)) == REFUSED
+        assert turned(L, P, 1, q=q, k=(every + 8, hk, every, token_k, True)) == REFUSED
+        assert turned(L, P, 1, q=q, k=(k0, hk, every + 8, token_k, True)) == REFUSED  # (strides of its own)

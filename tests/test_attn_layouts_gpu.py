@@ -86,3 +86,27 @@ def test_rotated_in_place_ranks_inside_a_token(marshalling, T):
     assert e.value.code == C.CAAT_ERR_INVALID_ARG
     torch.cuda.synchronize()
     assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("P,hq,hk", [(2, 4, 4), (3, 4, 1), (1, 4, 2)])
+def test_one_token_of_a_fused_projection(marshalling, P, hq, hk):
+    """A decoding step of one sequence, its q, k and v slices of one projection: q and k in place, and q in
+    place with k and v into a cache."""
+    dh = 64
+    torch.manual_seed(P)
+    qkv = torch.randn(P, 1, (hq + 2 * hk) * dh, device="cuda").to(BF)
+    q, k, v = (x.unflatten(-1, (-1, dh)) for x in qkv.split([hq * dh, hk * dh, hk * dh], -1))
+    v0 = v.clone()
+    turned_alike(q, k, 1)
+    freq, _ = C.caat_rope_frequencies(dh)
+    pos, slots = torch.tensor([3], dtype=torch.int32, device="cuda"), torch.tensor([3], device="cuda")
+    want = [torch.empty(x.shape, dtype=BF, device="cuda") for x in (q, k)]
+    C.caat_rope(q, k, pos, freq, q_out=want[0], k_out=want[1])
+    cache = [torch.zeros(P, 1, 9, hk, dh, dtype=BF, device="cuda") for _ in range(2)]
+    C.caat_rope_append(q, k, v, pos, slots, freq, *cache, q_out=q)
+    assert torch.equal(q, want[0]) and torch.equal(cache[0][:, 0, 3], want[1][:, 0]) and torch.equal(cache[1][:, 0, 3], v0[:, 0])
+    assert torch.equal(v, v0)
+    for c in cache:
+        c[:, 0, 3] = 0
+        assert not bool(c.any())
+    assert C.caat_get_device_status() == 0
