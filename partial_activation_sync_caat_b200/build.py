@@ -1,4 +1,4 @@
-"""Builds libcaat.so (the C-ABI library) in-tree with nvcc for sm_100a, and _marshal.so (the compiled
+"""Builds libcaat.so (the C-ABI library) in-tree with nvcc for sm_100a, and _marshal-*.so (the compiled
 half of the Python binding, against PyTorch's headers) with g++.
 
     python -m partial_activation_sync_caat_b200.build [--verbose-ptxas]
@@ -10,18 +10,19 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
 import sysconfig
 import tempfile
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libcaat.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 
 SOURCES = ["caat_api.cu", "attn_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -34,19 +35,30 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _deps():
-    files = [os.path.join(INCLUDE, "caat.h")]
-    for f in os.listdir(CSRC):
-        if f.endswith((".cu", ".cuh", ".h", ".cpp")):
-            files.append(os.path.join(CSRC, f))
-    return files
+def torch_version() -> str:
+    """The installed PyTorch's version, read from its files: importing it takes seconds."""
+    with open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")) as f:
+        return re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+
+
+def marshal_path(version: Optional[str] = None) -> str:
+    """The compiled marshalling for a PyTorch version (default: the installed one) and this interpreter.  It
+    reads their objects by the layouts that it was compiled for, so the name says which: under any other, there
+    is no such file."""
+    return os.path.join(PKG, f"_marshal-torch{version or torch_version()}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _newer(out: str, endings) -> bool:
+    files = [os.path.join(INCLUDE, "caat.h")] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(endings)]
+    return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in files)
+
+
+def marshal_up_to_date() -> bool:
+    return _newer(marshal_path(), (".cpp",))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _newer(LIB, (".cu", ".cuh", ".h")) and marshal_up_to_date()
 
 
 def _marshal_command(out: str) -> list:
@@ -71,7 +83,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         for src in SOURCES:
             cmd = base + ["-c", os.path.join(CSRC, src), "-o", os.path.join(objs, src + ".o")]
             jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-        cmd = _marshal_command(MARSHAL + ".tmp")
+        marshal = marshal_path()
+        cmd = _marshal_command(marshal + ".tmp")
         jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
         outs = [(cmd, p.communicate()[0], p.returncode) for cmd, p in jobs]
         if all(rc == 0 for _, _, rc in outs):
@@ -83,8 +96,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + text)
         if verbose_ptxas:
             sys.stderr.write(text)
+    os.replace(marshal + ".tmp", marshal)
     os.replace(tmp, LIB)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 

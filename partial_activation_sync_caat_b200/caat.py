@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import importlib.util
 import os
 import struct
 from typing import Optional
@@ -179,7 +180,7 @@ class AttnDecodeArgs(ctypes.Structure):
 
 
 # The attention block's calls are short enough for the marshalling to show: ordinary ones go through
-# _marshal.so, the others have their arguments packed in one go (native layout, the same as the structures above) and passed as bytes.
+# the compiled marshalling, the others have their arguments packed in one go (native layout, the same as the structures above) and passed as bytes.
 _PACK_ROPE = struct.Struct("@11P8q5ifI0P")
 _PACK_ATTN = struct.Struct("@5P2PPN2P8q5ifI0P")
 _PACK_ATTN_BWD = struct.Struct("@9P2PPN2P8q5ifI0P")
@@ -193,13 +194,18 @@ _marshal = None  # the compiled marshalling of the attention block's calls, boun
 
 
 def _bind_marshal(L):
-    """Imports _marshal.so and gives it the library's functions.  Built for another PyTorch or not at all,
-    it is left out: the calls are then marshalled here, which takes the host 5 us longer."""
+    """Loads the compiled marshalling and gives it the library's functions.  Built for another PyTorch or
+    interpreter, or not at all, it is left out: the calls are then marshalled here, which takes the host 5 us
+    longer."""
     global _marshal
+    from . import build
+    _marshal = None
+    name = __package__ + "._marshal"
+    spec = importlib.util.spec_from_file_location(name, build.marshal_path(torch.__version__))
     try:
-        from . import _marshal as m
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
     except ImportError:
-        _marshal = None
         return
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.caat_rope, L.caat_attn_forward, L.caat_attn_backward, L.caat_attn_decode, L.caat_attn_workspace_size)))
