@@ -35,9 +35,12 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def torch_version() -> str:
-    """The installed PyTorch's version, read from its files: importing it takes seconds."""
-    with open(os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "version.py")) as f:
+def torch_version() -> Optional[str]:
+    """The installed PyTorch's version, read from its files (importing it takes seconds); None without one."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    with open(os.path.join(os.path.dirname(spec.origin), "version.py")) as f:
         return re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
 
 
@@ -53,12 +56,13 @@ def _newer(out: str, endings) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(f) <= os.path.getmtime(out) for f in files)
 
 
-def marshal_up_to_date() -> bool:
-    return _newer(marshal_path(), (".cpp",))
-
-
 def up_to_date() -> bool:
-    return _newer(LIB, (".cu", ".cuh", ".h")) and marshal_up_to_date()
+    """Whether the library is (what the binding can do without is not asked for)."""
+    return _newer(LIB, (".cu", ".cuh", ".h"))
+
+
+def marshal_up_to_date() -> bool:
+    return torch_version() is None or _newer(marshal_path(), (".cpp",))
 
 
 def _marshal_command(out: str) -> list:
@@ -70,9 +74,38 @@ def _marshal_command(out: str) -> list:
             "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not verbose_ptxas and up_to_date():
-        return LIB
+def _start(cmd):
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _start_marshal():
+    """Starts the compiler on the compiled marshalling and returns what finishes it.  The binding can do without
+    (its calls then take the host longer), so no failure of this stops the library's build; a file of older
+    sources goes, since the structures of its calls may be others."""
+    if torch_version() is None:
+        return lambda: None
+    path = marshal_path()
+    cmd, job, why = [], None, ""
+    try:
+        cmd = _marshal_command(path + ".tmp")
+        job = _start(cmd)
+    except (OSError, RuntimeError) as e:
+        why = str(e)
+
+    def finish():
+        text = job.communicate()[0] if job else why
+        if job and job.returncode == 0:
+            os.replace(path + ".tmp", path)
+            return
+        for f in (path + ".tmp", path):
+            if os.path.exists(f):
+                os.remove(f)
+        sys.stderr.write("the compiled marshalling was not built; calls will be marshalled in Python:\n"
+                         + " ".join(cmd) + "\n" + text + "\n")
+    return finish
+
+
+def _build_library(verbose_ptxas: bool):
     tmp = LIB + ".tmp"
     base = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler",
             "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC, "-DCAAT_BUILD"]
@@ -82,10 +115,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         jobs = []
         for src in SOURCES:
             cmd = base + ["-c", os.path.join(CSRC, src), "-o", os.path.join(objs, src + ".o")]
-            jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-        marshal = marshal_path()
-        cmd = _marshal_command(marshal + ".tmp")
-        jobs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+            jobs.append((cmd, _start(cmd)))
         outs = [(cmd, p.communicate()[0], p.returncode) for cmd, p in jobs]
         if all(rc == 0 for _, _, rc in outs):
             cmd = base + ["-shared", "-o", tmp] + [os.path.join(objs, src + ".o") for src in SOURCES]
@@ -96,8 +126,18 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + text)
         if verbose_ptxas:
             sys.stderr.write(text)
-    os.replace(marshal + ".tmp", marshal)
-    os.replace(tmp, LIB)
+    return tmp
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    force = force or verbose_ptxas
+    finish = _start_marshal() if force or not marshal_up_to_date() else lambda: None
+    try:
+        tmp = _build_library(verbose_ptxas) if force or not up_to_date() else None
+    finally:
+        finish()
+    if tmp:  # last: whoever waits for the library finds the marshalling beside it
+        os.replace(tmp, LIB)
     return LIB
 
 
