@@ -12,10 +12,10 @@ import ctypes
 import importlib.util
 import os
 import struct
+import sys
 from typing import Optional
 
 import numpy as np
-import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libcaat.so")
@@ -191,15 +191,17 @@ _PACKED = {"caat_rope": (_PACK_ROPE, RopeArgs), "caat_attn_forward": (_PACK_ATTN
 _SIZE_MAX = ctypes.c_size_t(-1).value
 _lib = None
 _marshal = None  # the compiled marshalling of the attention block's calls, bound to the library
+_marshal_sought = False
 
 
 def _bind_marshal(L):
     """Loads the compiled marshalling and gives it the library's functions.  Built for another PyTorch or
     interpreter, or not at all, it is left out: the calls are then marshalled here, which takes the host 5 us
     longer."""
-    global _marshal
+    global _marshal, _marshal_sought
+    import torch
     from . import build
-    _marshal = None
+    _marshal, _marshal_sought = None, True
     name = __package__ + "._marshal"
     spec = importlib.util.spec_from_file_location(name, build.marshal_path(torch.__version__))
     try:
@@ -214,7 +216,9 @@ def _bind_marshal(L):
 
 def _fast():
     """The compiled marshalling (or None), after the library has been loaded."""
-    lib()
+    L = lib()
+    if not _marshal_sought:
+        _bind_marshal(L)
     return _marshal
 
 
@@ -291,8 +295,9 @@ def lib() -> ctypes.CDLL:
     L.caat_status_string.restype = ctypes.c_char_p
     L.caat_version.argtypes = []
     L.caat_version.restype = ctypes.c_char_p
-    _bind_marshal(L)
     _lib = L
+    if sys.modules.get("torch") is not None:  # else with the first call that needs it: host-only ones do not
+        _bind_marshal(L)
     return L
 
 
@@ -661,6 +666,7 @@ def caat_rope_frequencies(rot: int, theta: float = 10000.0, scaling: str = "none
 
 def _current(t, name):
     """Index of the tensor's device, which has to be the current one: the library queues there."""
+    import torch
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -671,6 +677,7 @@ def _current(t, name):
 
 def _raw_stream(stream, dev):
     if stream is None:
+        import torch
         return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{dev}")
@@ -770,6 +777,7 @@ def _rope_out(o, x, name, dtype, dev):
 
 
 def _rope(q, k, v, positions, slots, inv_freq, q_out, k_out, v_out, interleaved, backward, mscale, stream, timing):
+    import torch
     first = q if q is not None else k
     if first is None:
         raise ValueError("caat_rope: q and k are both None")
@@ -852,6 +860,7 @@ def caat_rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, *, q
 def _attn_qkv(q, k, v, cu_q, cu_k):
     """Checks of what the forward and the backward share: (device, what must outlive the call,
     addresses of q, k and v, addresses and count of the offsets, strides)."""
+    import torch
     dev = _current(q, "q")
     bf = torch.bfloat16
     q_ptr, qr, qt = _heads4(q, "q", bf, dev)
@@ -883,6 +892,7 @@ def caat_attn_forward(q, k, v, cu_q, out, *, cu_k=None, lse=None, scale: Optiona
             if code:
                 _check(code, "caat_attn_forward")
             return out
+    import torch
     dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     P, Tq, hq, dh = q.shape
     Tk, hk = k.shape[1:3]
@@ -914,6 +924,7 @@ def caat_attn_backward(q, k, v, out, lse, dout, cu_q, dq, dk, dv, *, cu_k=None, 
             if code:
                 _check(code, "caat_attn_backward")
             return dq, dk, dv
+    import torch
     dev, keep, qkv, cu, n, strides = _attn_qkv(q, k, v, cu_q, cu_k)
     bf = torch.bfloat16
     P, Tq, hq, dh = q.shape
@@ -951,6 +962,7 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
             if code:
                 _check(code, "caat_attn_decode")
             return out
+    import torch
     bf = torch.bfloat16
     dev = _current(q, "q")
     q_ptr, qr, qt = _heads4(q, "q", bf, dev)
