@@ -10,7 +10,7 @@ from partial_activation_sync_caat_b200 import caat as C
 
 from attn_util import check_grads
 from gpu_util import ensure_built
-from test_attn_gpu import forward, make
+from test_attn_gpu import backward, forward, make
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,37 @@ def test_gradients_run_after_run(P, hq, hk, dh, lens, klens):
     torch.cuda.synchronize()
     assert C.caat_get_device_status() == 0
     assert differ.tolist() == [0, 0, 0], f"runs with another dq, dk, dv: {differ.tolist()}"
+
+
+def test_long_work_lists_captured():
+    """More work items than a launch carries in its arguments: the lists travel through the workspace, and a graph
+    puts them there anew each time, whatever the workspace held."""
+    lens = [(11 * i) % 29 for i in range(500)]
+    d = make(1, 2, 1, 64, lens, seed=33)
+    want, lse_w = forward(d)
+    grads_w = backward(d, want, lse_w)
+    x = {n: d[n].cuda() for n in ("q", "k", "v", "dout")}
+    out, lse = torch.empty_like(want), torch.empty_like(lse_w)
+    grads = [torch.empty_like(x[n]) for n in ("q", "k", "v")]
+    T, n = d["cu_q"][-1], len(lens)
+    need = [C.caat_attn_workspace_size(T, T, n, 1, 2, 1, 64, v) for v in (C.CAAT_VARIANT_ATTN, C.CAAT_VARIANT_ATTN_BWD)]
+    assert need[0] > 0
+    ws = [C.alloc_workspace(b) for b in need]
+
+    def both():
+        C.caat_attn_forward(x["q"], x["k"], x["v"], d["cu_q"], out, lse=lse, workspace=ws[0])
+        C.caat_attn_backward(x["q"], x["k"], x["v"], out, lse, x["dout"], d["cu_q"], *grads, workspace=ws[1])
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for _ in range(3):
+        for t in (out, lse, *grads):
+            t.zero_()
+        for w in ws:
+            w.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, lse_w)
+        assert all(torch.equal(g, grads_w[n]) for g, n in zip(grads, ("dq", "dk", "dv")))
+    assert C.caat_get_device_status() == 0
