@@ -507,8 +507,8 @@ CAAT_API caat_status caat_rope_frequencies(int rot, double theta, int scaling, d
  *   rot        0 < rot <= dh; rot % 16 == 0 (interleaved: rot % 8 == 0)
  *   dh         dh % 8 == 0, dh <= 256
  * Outputs that are not in place must not overlap the inputs; a tensor turned in place must not share
- * elements with another one, nor with itself between ranks (slices of one projection do not).  Pointers
- * 16-byte aligned, positions 4, slots 8.
+ * elements with another one, nor with itself between ranks (slices of one projection do not); from one of
+ * other strides it must lie apart.  Pointers 16-byte aligned, positions 4, slots 8.
  */
 typedef struct caat_rope_args {
   const caat_bf16* q;
@@ -633,7 +633,10 @@ CAAT_API caat_status caat_attn_backward(const caat_attn_bwd_args* args);
  *                    never used, whatever they hold.
  *   out              device bf16 [P, B, heads_q * dh] contiguous; must not overlap the inputs
  *   workspace        caat_attn_workspace_size(B, capacity, ..., CAAT_VARIANT_ATTN_DECODE) bytes, 256-byte
- *                    aligned, NULL when that is 0; two calls that may overlap on the GPU need one each
+ *                    aligned, NULL when that is 0; two calls that may overlap on the GPU need one each.  It is
+ *                    0 where a cluster of CTAs takes each segment (sequence, rank, key head, 16 query heads), and
+ *                    is not for capacities above 16384, for few segments (fewer than 148 CTAs) of long capacity,
+ *                    and for more than 592 CTAs with less than 1 MiB of K and V each
  *   B                at most 4096
  *   dh, heads, scale as in caat_attn_forward
  * Deterministic; capturable.

@@ -978,7 +978,7 @@ def caat_attn_decode(q, k_cache, v_cache, lens, out, *, scale: Optional[float] =
             dh ** -0.5 if scale is None else scale, 0)
     ws, ws_ptr, ws_bytes = (None, 0, 0) if workspace is None else _workspace(workspace, 0, dev, stream)
     code = L.packed_caat_attn_decode(_PACK_ATTN_DECODE.pack(*head, ws_ptr, ws_bytes, *tail))
-    if code == CAAT_ERR_WORKSPACE and workspace is None:  # only few or very long sequences need one
+    if code == CAAT_ERR_WORKSPACE and workspace is None:  # where no cluster takes a sequence's heads
         need = L.caat_attn_workspace_size(B, cap, 0, P, hq, hk, dh, CAAT_VARIANT_ATTN_DECODE)
         ws, ws_ptr, ws_bytes = _workspace(None, need, dev, stream)
         code = L.packed_caat_attn_decode(_PACK_ATTN_DECODE.pack(*head, ws_ptr, ws_bytes, *tail))

@@ -194,7 +194,8 @@ void key_jobs(const int32_t* cu_q, const int32_t* cu_k, int n_seq, std::vector<c
 // CTAs that share the queries of a key tile (their fp32 sums are then joined by another kernel): enough
 // for two waves of the 148 SMs when ranks, key heads and tiles alone do not give them, but with 8 steps of 64
 // queries each at least (34 tokens, 4 ranks of 4 heads: 26.7 us with 16 empty or short parts, 16.4 without;
-// 606 tokens 45.1 | 28.7).
+// 606 tokens 45.1 | 28.7).  (148, here and below, and not the device's count: the workspace's size goes by the
+// same rules, and may be asked for where there is no GPU.)
 int dkv_splits(int64_t Tq, int64_t Tk, int P, int hq, int hk) {
   const int64_t units = std::max<int64_t>(Tk / caat::KA_TILE, 1) * P * hk;
   const int64_t steps = (Tq / caat::KB2_QT + 1) * (hq / hk);
@@ -530,7 +531,7 @@ caat_status caat_rope(const caat_rope_args* a) {
   const int64_t items = int64_t(a->P) * ((prm.q.heads + prm.k.heads) * per_head + prm.v.heads * (a->dh / 8));
   // Two items a thread keep more loads in flight for many tokens; for few, one a thread spreads them over
   // more SMs, and where a token has no more than 256 the second would be nobody's (T=3001, 176 items a
-  // token: 8.2 us | 9.1).
+  // token: 8.2 us | 9.1 in one run; 8.2 to 10.2 from run to run, as calls this short end in steps of 2 us).
   const bool few = items <= caat::KR_THREADS || a->T * ((items + 511) / 512) < 4 * int64_t(sms);
   const int per_cta = caat::KR_THREADS * (few ? 1 : 2);
   const unsigned gy = static_cast<unsigned>((items + per_cta - 1) / per_cta);

@@ -38,7 +38,8 @@
 namespace caat {
 
 // Every 8th pair of exponentials comes from a polynomial on the FMA units: the special-function units
-// (16 per clock and SM) bound a step.  T=8192, 32 heads: none 482 us, every 8th 462-472, every 4th 464-474.
+// (16 per clock and SM) bound a step.  T=8192, 32 heads, on a cool part: none 482 us, every 8th 461-472, every 4th
+// 464-474; at the power cap every 8th takes 554-563, and none, every 4th and every 16th 2-3% more.
 constexpr int KF_POLY = 8;
 constexpr int KF_STEP = 64;  // keys of a step
 constexpr int KF_ODD = 8;  // barriers of blocks to scrub: more than V blocks fit in the ring
