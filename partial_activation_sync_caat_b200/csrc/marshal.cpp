@@ -140,7 +140,7 @@ template <class Args>
 bool given_workspace(PyObject* o, int dev, Args* a) {
   if (o == Py_None) return true;
   const at::Tensor* t = tensor(o, dev);
-  if (!t) return false;
+  if (!t || !t->is_contiguous()) return false;  // (its elements say how long it is)
   a->workspace = t->data_ptr();
   a->ws_bytes = static_cast<size_t>(t->numel()) * t->element_size();
   return true;

@@ -110,3 +110,20 @@ def test_one_token_of_a_fused_projection(marshalling, P, hq, hk):
         c[:, 0, 3] = 0
         assert not bool(c.any())
     assert C.caat_get_device_status() == 0
+
+
+def test_workspaces_with_gaps_are_refused(marshalling):
+    """A workspace is taken for as long as its elements are many: one that is not contiguous is not."""
+    n = 64
+    q, k = (torch.zeros(1, n, h, 64, dtype=BF, device="cuda") for h in (2, 1))
+    out, lse = torch.zeros(1, n, 128, dtype=BF, device="cuda"), torch.zeros(1, 2, n, device="cuda")
+    grads = [torch.zeros_like(x) for x in (q, k, k)]
+    need = C.caat_attn_workspace_size(n, n, 1, 1, 2, 1, 64, C.CAAT_VARIANT_ATTN_BWD)
+    byte = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for ws in (byte.expand(need // 256 + 1, 256), C.alloc_workspace(2 * need)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            C.caat_attn_backward(q, k, k, out, lse, out, [0, n], *grads, workspace=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            C.caat_attn_forward(q, k, k, [0, n], out, workspace=ws)
+    torch.cuda.synchronize()
+    assert not bool(byte.any()) and C.caat_get_device_status() == 0
